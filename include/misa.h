@@ -78,7 +78,10 @@ typedef enum {
   MISA_OP_SCORE_TOPK_PAGED = 7,
   MISA_OP_RERANK_PAGED = 8,
   MISA_OP_SCORE_TOPK_FUSED = 9,
-  MISA_OP_HIER_FUSED = 10
+  MISA_OP_HIER_FUSED = 10,
+  MISA_OP_KV4_ATTENTION = 11,
+  MISA_OP_KV4_COMPACT = 12,
+  MISA_OP_KEYS_COMPACT_PAGED = 13
 } misa_op;
 
 /* Largest k' accepted by misa_hier_rerank (its candidates are ranked in shared memory). */
@@ -93,7 +96,8 @@ const char* misa_status_str(int status);
 /*
  * Workspace bytes needed by one call of `op` with these sizes (0 if it needs none).
  * Arguments an op does not use are ignored.  Sizes <= 0 give 0.  For MISA_OP_BLOCK_FILTER the
- * last argument carries m, the number of kept blocks (0 when m * B exceeds MISA_MAX_KP).
+ * last argument carries m, the number of kept blocks (0 when m * B exceeds MISA_MAX_KP).  The calls
+ * on 4-bit caches and compactions name what they put into these arguments themselves.
  */
 size_t misa_workspace_bytes(int op, int T, int L, int H_I, int B, int h, int topk, int kp);
 
@@ -327,6 +331,118 @@ misa_status misa_hier_topk_fused(const void* q, const float* w, const void* k, i
                                  const int32_t* n, const int32_t* heads, int T, int L, int H_I, int d,
                                  int h, int kp, int topk, int dtype, int32_t* idx, float* score_opt,
                                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention beside the indexer.
+ *
+ * The indexer selects tokens; these calls fill the caches its tokens live in, attend over them, and
+ * thin them out.  They serve d = 64 or 128 with H_q query heads over H_kv key and value heads (H_q a
+ * multiple of H_kv; query head h reads kv head h / (H_q / H_kv)).  Softmax is taken in fp32;
+ * lse is its natural log-sum, minus infinity for a row that attends to nothing, whose output is zero.
+ *
+ * Packed rows.  cu [S + 1] and, where a cache is involved, start [S] (int32, on the device) say which
+ * rows of a packed tensor belong to which sequence: row r of sequence b, cu[b] <= r < cu[b + 1], is
+ * its logical position start[b] + r - cu[b].  cu must not decrease and cu[0] >= 0; a sequence may be
+ * empty.  Rows outside [cu[0], cu[S]) are neither read nor written.
+ *
+ * Caches in 4 bits.  Every 16 elements of a row share a scale; an element is one of the 16 e2m1 values
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign) times it:
+ *   s_b = e4m3(max |x_i| / (6 g)),  code_i = e2m1(x_i / (s_b g)),  and x_i reads as code_i s_b g
+ * over the 16 elements i of block b, both conversions to nearest with ties to even, the divisions and
+ * 6 g in fp32; g is k_scale or v_scale, one positive fp32 number per tensor (1 suits blocks whose
+ * largest element lies between about 0.1 and 2688; larger elements saturate, NaN stores as 0, infinite
+ * elements as the largest value).  A block whose scale rounds to 0 stores zeros.
+ *   pool       : uint8 [num_pages][H_kv][2][page_size * 9 d / 16], 16-byte aligned; the slab of one
+ *                page, kv head and side (0 keys, 1 values) holds page_size code rows of d/2 bytes and
+ *                behind them page_size scale rows of d/16 e4m3 bytes.  Byte (d/8) c + 2 j + i of a code row
+ *                holds elements 16 j + 4 c + 2 i (low nibble) and the next (c < 4, j < d/16, i < 2).
+ *   page_size  : a multiple of 16, at most 1024 (else MISA_ERR_UNSUPPORTED)
+ *   page_table : [S or T][max_pages] int32, as for the paged key caches; the same tables can serve
+ *                both.  Ids outside [0, num_pages) are never dereferenced: rows are not written, read
+ *                as zero, and left out of the attention.
+ */
+
+/*
+ * Writes rows of k and v [rows][H_kv][d] (dtype; row strides ldk, ldv elements, multiples of 16 bytes;
+ * 16-byte aligned) into the cache at their logical positions.  Two rows of one call must not have the
+ * same place.  Positions that the page table does not reach are skipped.
+ */
+misa_status misa_kv4_append(const void* k, const void* v, int64_t ldk, int64_t ldv, int dtype, float k_scale,
+                            float v_scale, void* pool, int64_t num_pages, int page_size, const int32_t* page_table,
+                            int64_t max_pages, const int32_t* cu, const int32_t* start, int S, int rows, int H_kv,
+                            int d, void* stream);
+
+/*
+ * Reads rows of the cache back into k and v [rows][H_kv][d] (dtype, 16-byte aligned; for a chunk of a
+ * prompt that attends to what the cache already holds).  bf16 holds code_i s_b exactly.
+ */
+misa_status misa_kv4_read(const void* pool, int64_t num_pages, int page_size, const int32_t* page_table,
+                          int64_t max_pages, const int32_t* cu, const int32_t* start, int S, int rows, int H_kv, int d,
+                          int dtype, float k_scale, float v_scale, void* k, void* v, void* stream);
+
+/*
+ * Attention of one query token per sequence over its 4-bit cache:
+ *   out[t, h] = sum_i softmax_i(scale q[t, h] . k_i) v_i   over i < n_t, or over i in idx[t].
+ *   q, out     : [T][H_q][d], dtype (bf16, or fp32 computed to fp32's accuracy); 16-byte aligned
+ *   idx        : [T][P] tokens to attend to, in any order (misa_score_topk and the other selections
+ *                write such lists), or NULL for the whole prefix.  Entries < 0 or >= n_t are empty slots;
+ *                a token named twice counts twice.
+ *   lse_opt    : out [T][H_q] fp32, or NULL
+ *   acc_opt    : [T][ld_acc] fp32, or NULL: acc[t][i] += sum over the H_q heads of token i's softmax
+ *                weight (ld_acc >= L; other entries are not touched)
+ *   ws         : misa_workspace_bytes(MISA_OP_KV4_ATTENTION, T, L, H_q, H_kv, d, P or 0, 1 with acc_opt
+ *                else 0) bytes; with acc_opt it holds the logits, 4 H_q bytes per query and token
+ */
+misa_status misa_kv4_attention(const void* q, const void* pool, int64_t num_pages, int page_size,
+                               const int32_t* page_table, int64_t max_pages, const int32_t* n, const int32_t* idx,
+                               int T, int L, int P, int H_q, int H_kv, int d, int dtype, float scale, float k_scale,
+                               float v_scale, void* out, float* lse_opt, float* acc_opt, int64_t ld_acc, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * Which tokens stay when caches are thinned to `keep` tokens by the attention weight they have gathered
+ * (acc of misa_kv4_attention).  Prefixes of at most keep tokens stay whole; of a longer one stay the
+ * first `sink`, the last `recent` (sink + recent <= keep), and of those between the ones with the
+ * largest acc (ties: lower token; NaN counts as the smallest).
+ *   acc         : [T][ld_acc] fp32, entries i < n_t are read (ld_acc >= L)
+ *   idx         : out [T][keep] the tokens that stay, ascending, -1 behind the last
+ *   n_out       : out [T] min(n_t, keep)
+ *   acc_out_opt : out [T][ld_out] (ld_out >= keep): acc of the tokens that stay, in the order of idx,
+ *                 then zeros to the end of the row; must not overlap acc.  Or NULL.
+ */
+misa_status misa_evict_select(const float* acc, int64_t ld_acc, const int32_t* n, int T, int L, int keep, int sink,
+                              int recent, int32_t* idx, int32_t* n_out, float* acc_out_opt, int64_t ld_out,
+                              void* stream);
+
+/*
+ * Closes up caches after misa_evict_select, in place: row idx[t][j] of sequence t moves to row j, for
+ * the 4-bit cache or the indexer's paged keys (pool [num_pages][page_size][128] of dtype).  idx is
+ * ascending with -1 behind the last, as misa_evict_select writes it.  Rows from the number kept on keep
+ * their contents; block means of the keys are pooled again with misa_pool_keys_paged.  The pages of the
+ * T sequences must be theirs alone.
+ *   ws : misa_workspace_bytes(MISA_OP_KV4_COMPACT, T, 0, H_kv, 0, d, keep, 0), and
+ *        misa_workspace_bytes(MISA_OP_KEYS_COMPACT_PAGED, T, 0, 0, 0, bytes of a key row, keep, 0) bytes
+ */
+misa_status misa_kv4_compact(void* pool, int64_t num_pages, int page_size, const int32_t* page_table,
+                             int64_t max_pages, const int32_t* idx, int T, int keep, int H_kv, int d, void* ws,
+                             size_t ws_bytes, void* stream);
+misa_status misa_keys_compact_paged(void* pool, int64_t num_pages, int page_size, const int32_t* page_table,
+                                    int64_t max_pages, const int32_t* idx, int T, int keep, int d, int dtype, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/*
+ * Causal attention of packed prompts.  Sequence b has queries cu_q[b] .. cu_q[b + 1] of q and keys
+ * cu_k[b] .. cu_k[b + 1] of k and v, its queries being its last tokens: query i of it sees its keys
+ * j <= i + (keys - queries).  With cu_k = cu_q that is a whole prompt; with more keys it is a chunk that
+ * ends a longer one; queries before the first key see nothing.
+ *   q      : [Tq][H_q][d] at row stride ldq elements; k, v : [Tk][H_kv][d] at ldk, ldv (multiples of 8
+ *            elements, so the views of one fused projection serve; 16-byte aligned); bf16 only
+ *   out    : [Tq][H_q][d] bf16;  lse_opt : [Tq][H_q] fp32, or NULL
+ * Rows of other sequences never reach a sequence's outputs, whatever they hold.
+ */
+misa_status misa_prompt_attention(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
+                                  const int32_t* cu_q, const int32_t* cu_k, int S, int Tq, int Tk, int H_q, int H_kv,
+                                  int d, int dtype, float scale, void* out, float* lse_opt, void* stream);
 
 /*
  * Device-side status of the calls made so far on the current device.  The tensor-core kernels

@@ -31,7 +31,8 @@ LIB_PATH = os.path.join(PKG, "libmisa_checked.so" if os.environ.get("MISA_LIBRAR
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_BAD_INDEX = range(7)
 BF16, F32 = 0, 1
 (OP_ROUTE, OP_SCORE_TOPK, OP_RERANK, OP_DENSE_TOPK, OP_TOPK_SELECT, OP_BLOCK_FILTER, OP_ROUTE_PAGED,
- OP_SCORE_TOPK_PAGED, OP_RERANK_PAGED, OP_SCORE_TOPK_FUSED, OP_HIER_FUSED) = range(11)
+ OP_SCORE_TOPK_PAGED, OP_RERANK_PAGED, OP_SCORE_TOPK_FUSED, OP_HIER_FUSED, OP_KV4_ATTENTION, OP_KV4_COMPACT,
+ OP_KEYS_COMPACT_PAGED) = range(14)
 MAX_KP = 16384
 
 if not os.path.exists(LIB_PATH):
@@ -45,7 +46,7 @@ class MisaError(RuntimeError):
 
 
 def _setup(lib):
-    P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    P, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     sigs = {
         "misa_version": ([], i32),
         "misa_device_check": ([], i32),
@@ -71,6 +72,15 @@ def _setup(lib):
                                     P], i32),
         "misa_score_topk_fused": ([P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, P, P, sz, P], i32),
         "misa_hier_topk_fused": ([P, P, P, i64, P, P, i32, i32, i32, i32, i32, i32, i32, i32, P, P, P, sz, P], i32),
+        "misa_kv4_append": ([P, P, i64, i64, i32, f32, f32, P, i64, i32, P, i64, P, P, i32, i32, i32, i32, P], i32),
+        "misa_kv4_read": ([P, i64, i32, P, i64, P, P, i32, i32, i32, i32, i32, f32, f32, P, P, P], i32),
+        "misa_kv4_attention": ([P, P, i64, i32, P, i64, P, P, i32, i32, i32, i32, i32, i32, i32, f32, f32, f32, P, P,
+                                P, i64, P, sz, P], i32),
+        "misa_evict_select": ([P, i64, P, i32, i32, i32, i32, i32, P, P, P, i64, P], i32),
+        "misa_kv4_compact": ([P, i64, i32, P, i64, P, i32, i32, i32, i32, P, sz, P], i32),
+        "misa_keys_compact_paged": ([P, i64, i32, P, i64, P, i32, i32, i32, i32, P, sz, P], i32),
+        "misa_prompt_attention": ([P, P, P, i64, i64, i64, P, P, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P],
+                                  i32),
     }
     for name, (args, res) in sigs.items():
         f = getattr(lib, name)
@@ -781,3 +791,253 @@ def misa_indexer_paged(q, w, pool, page_table, kbar, n, B: int, h: int, topk: in
                                     stream=stream)
     idx, vals = misa_hier_rerank_paged(q, w, pool, page_table, n, cand, topk, L=L, ws=ws, stream=stream)
     return {"idx": idx, "vals": vals, "heads": heads, "cand": cand}
+
+
+# ---- attention beside the indexer: 4-bit caches, their attention and eviction, prompt attention ------
+
+def misa_kv4_pool(num_pages: int, page_size: int, H_kv: int, d: int, device="cuda") -> torch.Tensor:
+    """An empty pool of 4-bit key and value pages, uint8 [num_pages, H_kv, 2, page_size * 9 d / 16]."""
+    if d not in (64, 128) or page_size < 16 or page_size % 16:
+        raise ValueError(f"a 4-bit pool needs d of 64 or 128 and pages of a multiple of 16 rows, got d = {d}, "
+                         f"page_size = {page_size}")
+    return torch.zeros((num_pages, H_kv, 2, page_size * 9 * d // 16), dtype=torch.uint8, device=device)
+
+
+def _kv4_geometry(pool, page_table, rows: int, d: int):
+    """(num_pages, H_kv, page_size, max_pages) of a 4-bit pool with heads of d elements."""
+    s = pool.shape
+    if len(s) != 4 or s[2] != 2 or s[3] <= 0 or (s[3] * 16) % (9 * d) != 0:
+        raise ValueError(f"pool must be [num_pages, H_kv, 2, page_size * {9 * d} / 16], got {tuple(s)}")
+    _matrix(page_table, "page_table", rows)
+    return s[0], s[1], s[3] * 16 // (9 * d), page_table.shape[1]
+
+
+def _packed_rows(t, name: str, dtype=None):
+    """Row stride in elements of packed rows [rows, H, d]: rows may be strided (a slice of a fused
+    projection), the elements of a row may not."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, H, d], got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, H, d = t.shape
+    if t.numel() == 0 or (rows == 1 and t[0].is_contiguous()):
+        return H * d
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != d) or t.stride(0) < H * d or t.stride(0) * t.element_size() % 16:
+        raise ValueError(f"{name} must have contiguous rows at a stride of a multiple of 16 bytes, got strides "
+                         f"{tuple(t.stride())}")
+    return t.stride(0)
+
+
+def _packed(cu, start, name: str = "cu") -> int:
+    """Number of sequences of cu [S + 1] (and start [>= S])."""
+    if cu.dim() != 1 or cu.shape[0] < 1:
+        raise ValueError(f"{name} must be [S + 1], got {tuple(cu.shape)}")
+    S = cu.shape[0] - 1
+    if start is not None and (start.dim() != 1 or start.shape[0] < S):
+        raise ValueError(f"start must be [>= {S}], got {tuple(start.shape)}")
+    return S
+
+
+def misa_kv4_append(k, v, pool, page_table, cu, start, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """Write packed rows k, v [rows, H_kv, d] into a 4-bit cache: row r of sequence b (cu[b] <= r <
+    cu[b + 1]) at its logical position start[b] + r - cu[b].  k_scale and v_scale: one factor per
+    tensor, the same in every call on this cache."""
+    ldk, ldv = _packed_rows(k, "k"), _packed_rows(v, "v", k.dtype)
+    if k.shape != v.shape:
+        raise ValueError(f"k and v must have one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
+    rows, H_kv, d = k.shape
+    S = _packed(cu, start)
+    num_pages, Hp, page_size, max_pages = _kv4_geometry(pool, page_table, S, d)
+    if Hp != H_kv:
+        raise ValueError(f"the pool holds {Hp} kv heads, k has {H_kv}")
+    _need(pool, "pool", torch.uint8)
+    _need(page_table, "page_table", torch.int32)
+    _need(cu, "cu", torch.int32)
+    _need(start, "start", torch.int32)
+    _on_device(k, v, pool, page_table, cu, start)
+    _check("misa_kv4_append", _lib.misa_kv4_append(
+        _p(k), _p(v), ldk, ldv, _dtype_code(k), k_scale, v_scale, _p(pool), num_pages, page_size, _p(page_table),
+        max_pages, _p(cu), _p(start), S, rows, H_kv, d, _stream(stream)))
+
+
+def misa_kv4_read(pool, page_table, cu, start, rows: int, d: int, dtype=torch.bfloat16, k_scale: float = 1.0,
+                  v_scale: float = 1.0, k=None, v=None, stream=None):
+    """Rows of a 4-bit cache as packed k, v [rows, H_kv, d] (bf16 or fp32); the inverse of misa_kv4_append.
+    Rows outside [cu[0], cu[S]) of given k and v are left as they are."""
+    S = _packed(cu, start)
+    num_pages, H_kv, page_size, max_pages = _kv4_geometry(pool, page_table, S, d)
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None and tuple(t.shape) != (rows, H_kv, d):
+            raise ValueError(f"{name} must be {[rows, H_kv, d]}, got {tuple(t.shape)}")
+    _need(pool, "pool", torch.uint8)
+    _need(page_table, "page_table", torch.int32)
+    _need(cu, "cu", torch.int32)
+    _need(start, "start", torch.int32)
+    _need_opt(k, "k", dtype)
+    _need_opt(v, "v", dtype)
+    _on_device(pool, page_table, cu, start, k, v)
+    if k is None:
+        k = torch.empty((rows, H_kv, d), dtype=dtype, device=pool.device)
+    if v is None:
+        v = torch.empty((rows, H_kv, d), dtype=dtype, device=pool.device)
+    _check("misa_kv4_read", _lib.misa_kv4_read(
+        _p(pool), num_pages, page_size, _p(page_table), max_pages, _p(cu), _p(start), S, rows, H_kv, d,
+        _dtype_code(k), k_scale, v_scale, _p(k), _p(v), _stream(stream)))
+    return k, v
+
+
+def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None, scale: Optional[float] = None,
+                       k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None, want_lse: bool = False,
+                       acc=None, ws: Optional[Workspace] = None, stream=None):
+    """Attention of one query token per sequence, q [T, H_q, d] (bf16 or fp32), over its 4-bit cache:
+    over the whole prefix, or with idx [T, P] over the tokens listed there (the indexer's selection, -1
+    for empty slots) -> (out [T, H_q, d], lse [T, H_q] or None).  scale defaults to 1 / sqrt(d).  acc
+    [T, >= L] fp32: every token's softmax weight, summed over the heads, is added to it."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, H_q, d], got {tuple(q.shape)}")
+    T, H_q, d = q.shape
+    num_pages, H_kv, page_size, max_pages = _kv4_geometry(pool, page_table, T, d)
+    if L is None:  # the longest prefix that the table (and acc) can hold
+        L = max_pages * page_size if acc is None else min(max_pages * page_size, acc.shape[-1])
+    if n.dim() != 1 or n.shape[0] < T:
+        raise ValueError(f"n must be [>= {T}], got {tuple(n.shape)}")
+    if idx is not None:
+        _matrix(idx, "idx", T)
+    if out is not None and tuple(out.shape) != (T, H_q, d):
+        raise ValueError(f"out must be {[T, H_q, d]}, got {tuple(out.shape)}")
+    if lse is not None:
+        _matrix(lse, "lse", T, H_q)
+    if acc is not None:
+        _matrix(acc, "acc", T, min_cols=L)
+    _need(q, "q")
+    _need(pool, "pool", torch.uint8)
+    _need(page_table, "page_table", torch.int32)
+    _need(n, "n", torch.int32)
+    _need_opt(idx, "idx", torch.int32)
+    _need_opt(out, "out", q.dtype)
+    _need_opt(lse, "lse", torch.float32)
+    _need_opt(acc, "acc", torch.float32)
+    _on_device(q, pool, page_table, n, idx, out, lse, acc)
+    P = 0 if idx is None else idx.shape[1]
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((T, H_q), dtype=torch.float32, device=q.device)
+    nbytes = misa_workspace_bytes(OP_KV4_ATTENTION, T, L, H_q, H_kv, d, P, int(acc is not None))
+    buf = _ws(ws, q.device, stream).get(nbytes, stream)
+    _check("misa_kv4_attention", _lib.misa_kv4_attention(
+        _p(q), _p(pool), num_pages, page_size, _p(page_table), max_pages, _p(n), _p(idx), T, L, P, H_q, H_kv, d,
+        _dtype_code(q), d ** -0.5 if scale is None else scale, k_scale, v_scale, _p(out), _p(lse), _p(acc),
+        0 if acc is None else acc.shape[1], _p(buf), nbytes, _stream(stream)))
+    return out, lse
+
+
+def misa_evict_select(acc, n, keep: int, sink: int = 0, recent: int = 0, L: Optional[int] = None, idx=None,
+                      n_out=None, acc_out=None, want_acc: bool = False, stream=None):
+    """Tokens that stay when every cache is thinned to `keep` by summed attention weight acc [T, >= L]:
+    the first `sink`, the last `recent`, and the heaviest of the others -> (idx [T, keep] ascending and
+    -1 padded, n_out [T], acc_out [T, >= keep] the weights in that order and zeros behind them, or None)."""
+    if acc.dim() != 2:
+        raise ValueError(f"acc must be [T, ld], got {tuple(acc.shape)}")
+    T, ld = acc.shape
+    L = ld if L is None else L
+    if n.dim() != 1 or n.shape[0] < T:
+        raise ValueError(f"n must be [>= {T}], got {tuple(n.shape)}")
+    if idx is not None:
+        _matrix(idx, "idx", T, keep)
+    if n_out is not None and (n_out.dim() != 1 or n_out.shape[0] < T):
+        raise ValueError(f"n_out must be [>= {T}], got {tuple(n_out.shape)}")
+    if acc_out is not None:
+        _matrix(acc_out, "acc_out", T, min_cols=keep)
+    _need(acc, "acc", torch.float32)
+    _need(n, "n", torch.int32)
+    _need_opt(idx, "idx", torch.int32)
+    _need_opt(n_out, "n_out", torch.int32)
+    _need_opt(acc_out, "acc_out", torch.float32)
+    _on_device(acc, n, idx, n_out, acc_out)
+    if idx is None:
+        idx = torch.empty((T, keep), dtype=torch.int32, device=acc.device)
+    if n_out is None:
+        n_out = torch.empty((T,), dtype=torch.int32, device=acc.device)
+    if acc_out is None and want_acc:
+        acc_out = torch.empty((T, keep), dtype=torch.float32, device=acc.device)
+    _check("misa_evict_select", _lib.misa_evict_select(
+        _p(acc), ld, _p(n), T, L, keep, sink, recent, _p(idx), _p(n_out), _p(acc_out),
+        0 if acc_out is None else acc_out.shape[1], _stream(stream)))
+    return idx, n_out, acc_out
+
+
+def misa_kv4_compact(pool, page_table, idx, d: int, ws: Optional[Workspace] = None, stream=None) -> None:
+    """Close up a 4-bit cache in place: row idx[t, j] of sequence t moves to row j (idx [T, keep]
+    ascending, -1 padded, as misa_evict_select gives it)."""
+    if idx.dim() != 2:
+        raise ValueError(f"idx must be [T, keep], got {tuple(idx.shape)}")
+    T, keep = idx.shape
+    num_pages, H_kv, page_size, max_pages = _kv4_geometry(pool, page_table, T, d)
+    _need(pool, "pool", torch.uint8)
+    _need(page_table, "page_table", torch.int32)
+    _need(idx, "idx", torch.int32)
+    _on_device(pool, page_table, idx)
+    nbytes = misa_workspace_bytes(OP_KV4_COMPACT, T, 0, H_kv, 0, d, keep)
+    buf = _ws(ws, pool.device, stream).get(nbytes, stream)
+    _check("misa_kv4_compact", _lib.misa_kv4_compact(
+        _p(pool), num_pages, page_size, _p(page_table), max_pages, _p(idx), T, keep, H_kv, d, _p(buf), nbytes,
+        _stream(stream)))
+
+
+def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = None, stream=None) -> None:
+    """misa_kv4_compact for the indexer's paged keys, pool [num_pages, page_size, 128] (bf16 or fp32).
+    Block means are to be pooled again (misa_pool_keys_paged)."""
+    if pool.dim() != 3:
+        raise ValueError(f"pool must be [num_pages, page_size, d], got {tuple(pool.shape)}")
+    if idx.dim() != 2:
+        raise ValueError(f"idx must be [T, keep], got {tuple(idx.shape)}")
+    T, keep = idx.shape
+    _matrix(page_table, "page_table", T)
+    _need(pool, "pool")
+    _need(page_table, "page_table", torch.int32)
+    _need(idx, "idx", torch.int32)
+    _on_device(pool, page_table, idx)
+    num_pages, page_size, d = pool.shape
+    nbytes = misa_workspace_bytes(OP_KEYS_COMPACT_PAGED, T, 0, 0, 0, d * pool.element_size(), keep)
+    buf = _ws(ws, pool.device, stream).get(nbytes, stream)
+    _check("misa_keys_compact_paged", _lib.misa_keys_compact_paged(
+        _p(pool), num_pages, page_size, _p(page_table), page_table.shape[1], _p(idx), T, keep, d, _dtype_code(pool),
+        _p(buf), nbytes, _stream(stream)))
+
+
+def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, lse=None,
+                          want_lse: bool = False, stream=None):
+    """Causal attention of packed prompts, q [Tq, H_q, d] and k, v [Tk, H_kv, d] in bf16: sequence b has
+    queries cu_q[b] .. cu_q[b + 1] and keys cu_k[b] .. cu_k[b + 1] (cu_k defaults to cu_q), its queries
+    being its last tokens -> (out [Tq, H_q, d], lse [Tq, H_q] or None).  scale defaults to 1 / sqrt(d).
+    Rows of q, k and v may be strided (views of a fused projection); rows of given out and lse outside
+    the sequences are left as they are."""
+    ldq, ldk, ldv = (_packed_rows(t, name, torch.bfloat16) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    Tq, H_q, d = q.shape
+    Tk, H_kv, dk = k.shape
+    if k.shape != v.shape or dk != d:
+        raise ValueError(f"k and v must be [Tk, H_kv, {d}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    cu_k = cu_q if cu_k is None else cu_k
+    S = _packed(cu_q, None, "cu_q")
+    if cu_k.shape != cu_q.shape:
+        raise ValueError(f"cu_k must be {list(cu_q.shape)}, got {tuple(cu_k.shape)}")
+    if out is not None and tuple(out.shape) != (Tq, H_q, d):
+        raise ValueError(f"out must be {[Tq, H_q, d]}, got {tuple(out.shape)}")
+    if lse is not None and tuple(lse.shape) != (Tq, H_q):
+        raise ValueError(f"lse must be {[Tq, H_q]}, got {tuple(lse.shape)}")
+    _need(cu_q, "cu_q", torch.int32)
+    _need(cu_k, "cu_k", torch.int32)
+    _need_opt(out, "out", torch.bfloat16)
+    _need_opt(lse, "lse", torch.float32)
+    _on_device(q, k, v, cu_q, cu_k, out, lse)
+    if out is None:
+        out = torch.empty((Tq, H_q, d), dtype=torch.bfloat16, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((Tq, H_q), dtype=torch.float32, device=q.device)
+    _check("misa_prompt_attention", _lib.misa_prompt_attention(
+        _p(q), _p(k), _p(v), ldq, ldk, ldv, _p(cu_q), _p(cu_k), S, Tq, Tk, H_q, H_kv, d, BF16,
+        d ** -0.5 if scale is None else scale, _p(out), _p(lse), _stream(stream)))
+    return out, lse

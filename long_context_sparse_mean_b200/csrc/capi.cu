@@ -142,7 +142,8 @@ namespace {
 bool read_bad_ids(unsigned int* out) {
   for (int i = 0; i < misa::kBadIdKinds; ++i) out[i] = 0;
   return misa::read_and_clear_bad_ids_score(out) && misa::read_and_clear_bad_ids_paged(out) &&
-         misa::read_and_clear_bad_ids_block_filter(out) && misa::read_and_clear_bad_ids_rerank_tc(out);
+         misa::read_and_clear_bad_ids_block_filter(out) && misa::read_and_clear_bad_ids_rerank_tc(out) &&
+         misa::read_and_clear_bad_ids_kv4_cache(out) && misa::read_and_clear_bad_ids_kv4_attn(out);
 }
 }  // namespace
 
@@ -204,6 +205,13 @@ size_t misa_workspace_bytes(int op, int T, int L, int H_I, int B, int h, int top
       return T > 0 && L > 0 && misa::fused_cap(topk) > 0 ? align_up(misa::fused_ws_bytes(T, L, topk)) : 0;
     case MISA_OP_HIER_FUSED:
       return hier_fused_ws(T, L, kp);
+    case MISA_OP_KV4_ATTENTION:  // H_I query heads, B kv heads, h head width, topk selected tokens, kp weights
+      if (T <= 0 || L <= 0 || H_I <= 0 || B <= 0 || H_I % B != 0 || h <= 0) return 0;
+      return misa::kv4_attention_ws_bytes(T, topk > 0 ? topk : L, H_I, B, h, kp != 0);
+    case MISA_OP_KV4_COMPACT:  // H_I kv heads, h head width, topk kept tokens
+      return T > 0 && H_I > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, (int64_t)H_I * 2 * (9 * h / 16)) : 0;
+    case MISA_OP_KEYS_COMPACT_PAGED:  // h bytes of a key row, topk kept tokens
+      return T > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, h) : 0;
     default:
       return 0;
   }

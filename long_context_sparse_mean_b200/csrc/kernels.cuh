@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "kv4.cuh"
 #include "select.cuh"
 
 namespace misa {
@@ -197,5 +198,38 @@ void launch_pool_paged(DType dt, const void* pool, int64_t num_pages, int page_s
 // pm[t] = mean of the last block of query t's prefix (full or partial; untouched for an empty prefix).
 void launch_partial_mean_paged(DType dt, const void* pool, int64_t num_pages, int page_size, const int32_t* table,
                                int64_t max_pages, const int32_t* n, int T, int L, int B, float* pm, cudaStream_t s);
+
+// Caches held in 4 bits (kv4_cache.cu; format and Kv4Pool in kv4.cuh).  Packed rows [rows] belong to
+// sequence b for cu[b] <= r < cu[b + 1] and to its logical positions start[b] + r - cu[b].
+void launch_kv4_append(DType dt, const void* k, const void* v, int64_t ldk, int64_t ldv, const Kv4Pool& pool,
+                       const int32_t* cu, const int32_t* start, int S, int rows, float kg, float vg, cudaStream_t s);
+void launch_kv4_read(DType dt, const Kv4Pool& pool, const int32_t* cu, const int32_t* start, int S, int rows,
+                     float kg, float vg, void* k, void* v, cudaStream_t s);
+// Closes up the rows of every sequence in place: row idx[t, j] moves to row j (idx ascending, -1 behind
+// the last).  Rows of a page are rb bytes in each of `slabs` slabs of slab_bytes, and behind those
+// page_size scale rows of sb bytes (0, 4 or 8).
+size_t compact_ws_bytes(int T, int keep, int64_t row_bytes);
+void launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, int rb, int sb, const int32_t* idx,
+                         int T, int keep, void* ws, cudaStream_t s);
+
+// Attention of query t over its sequence's tokens in a 4-bit cache, or over the tokens idx[t][0 .. P)
+// (kv4_attn.cu).  acc (optional): acc[t, i] += sum over heads of token i's weight.
+size_t kv4_attention_ws_bytes(int T, int P, int Hq, int Hkv, int d, bool weights);
+void launch_kv4_attention(DType dt, const void* q, const Kv4Pool& pool, const int32_t* n, const int32_t* idx, int T,
+                          int L, int P, int Hq, float scale, float k_scale, float v_scale, void* out, float* lse,
+                          float* acc, int64_t ld_acc, void* ws, cudaStream_t s);
+
+// The tokens that stay when caches are thinned by summed attention weight (evict.cu).
+void launch_evict_select(const float* acc, int64_t ld, const int32_t* n, int T, int L, int keep, int sink, int recent,
+                         int32_t* idx, int32_t* n_out, float* acc_out, int64_t ld_out, cudaStream_t s);
+
+// Causal attention of packed prompts (prompt.cu): q [Tq][Hq][d], k and v [Tk][Hkv][d] at row strides
+// ldq, ldk, ldv; query i of sequence b sees keys j <= i + (keys - queries of b).
+void launch_prompt_attention(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
+                             const int32_t* cu_q, const int32_t* cu_k, int S, int Tq, int Tk, int Hq, int Hkv, int d,
+                             float scale, void* out, float* lse, cudaStream_t s);
+
+bool read_and_clear_bad_ids_kv4_cache(unsigned int* out);
+bool read_and_clear_bad_ids_kv4_attn(unsigned int* out);
 
 }  // namespace misa

@@ -1,0 +1,107 @@
+"""The calls of a serving loop together: a prompt is attended to and written to the 4-bit cache, decode steps
+select tokens with the indexer and attend to them, the caches are thinned by the weights they gathered, and
+decoding goes on over what is left."""
+import numpy as np
+import pytest
+import torch
+
+import attention_ref as R
+from gpu_common import host, lib
+
+pytestmark = pytest.mark.gpu
+
+
+def cuda(x, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def test_prompt_decode_evict_decode():
+    M = lib()
+    rng = np.random.default_rng(21)
+    T, Hq, Hkv, d, page, H_I, B, h, topk = 3, 16, 2, 128, 64, 16, 32, 4, 64
+    lens = [700, 233, 512]
+    per = -(-(max(lens) + 8) // page)
+    total = T * per
+    table_h = rng.permutation(total).reshape(T, per).astype(np.int32)
+    table = cuda(table_h)
+    pool, keys = M.misa_kv4_pool(total, page, Hkv, d), torch.zeros(total, page, 128, dtype=torch.bfloat16, device="cuda")
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    rows = int(cu[-1])
+    randn = lambda *s: cuda(rng.standard_normal(s).astype(np.float32), torch.bfloat16)  # noqa: E731
+    q, k, v, ik = randn(rows, Hq, d), randn(rows, Hkv, d), randn(rows, Hkv, d), randn(rows, 128)
+
+    # the prompt: attention in bf16, then the cache; the second half of it as a chunk over what was cached
+    out, _ = M.misa_prompt_attention(q, k, v, cuda(cu))
+    zero = cuda(np.zeros(T, np.int32))
+    M.misa_kv4_append(k, v, pool, table, cuda(cu), zero)
+    kb, vb = M.misa_kv4_read(pool, table, cuda(cu), zero, rows, d)
+    half = [n // 2 for n in lens]
+    cu_h = np.concatenate([[0], np.cumsum([n - a for n, a in zip(lens, half)])]).astype(np.int32)
+    qh = torch.cat([q[cu[b] + half[b]:cu[b + 1]] for b in range(T)])
+    chunk, _ = M.misa_prompt_attention(qh, kb, vb, cuda(cu_h), cuda(cu))
+    for b in range(T):
+        m, n = lens[b] - half[b], lens[b]
+        seen = np.arange(n)[None] <= (np.arange(m) + n - m)[:, None]
+        kk, vv, qq = (host(x.float()) for x in (kb[cu[b]:cu[b + 1]], vb[cu[b]:cu[b + 1]], qh[cu_h[b]:cu_h[b + 1]]))
+        want, _, p = R.attend(qq, kk, vv, d ** -0.5, seen)
+        tol, _ = R.attend_tolerance(qq, kk, vv, d ** -0.5, p, "bf16", 2.0 ** -8)
+        assert np.all(np.abs(host(chunk[cu_h[b]:cu_h[b + 1]].float()) - want) <= tol)
+        pos = torch.arange(lens[b], device="cuda")
+        keys[table[b].long()[pos // page], pos % page] = ik[cu[b]:cu[b + 1]]
+
+    n = cuda(np.array(lens, np.int32))
+    acc = torch.zeros(T, per * page, device="cuda")
+    acc_ref = np.zeros((T, per * page))
+    nh = np.array(lens)
+
+    def step():
+        """One decode step of every sequence; checks attention against the cache's own values."""
+        nonlocal nh
+        one, k1, v1, ik1 = randn(T, Hq, d), randn(T, Hkv, d), randn(T, Hkv, d), randn(T, 128)
+        M.misa_kv4_append(k1, v1, pool, table, cuda(np.arange(T + 1, dtype=np.int32)), n)
+        for t in range(T):
+            keys[table_h[t, nh[t] // page], nh[t] % page] = ik1[t]
+        n.add_(1)
+        nh = nh + 1
+        kbar = M.misa_pool_keys_paged(keys, table, B)
+        iq, iw = randn(T, H_I, 128), cuda(rng.standard_normal((T, H_I)).astype(np.float32))
+        sel = M.misa_indexer_paged(iq, iw, keys, table, kbar, n, B, h, topk)
+        o, lse = M.misa_kv4_attention(one, pool, table, n, idx=sel["idx"], acc=acc, want_lse=True)
+        pl = host(pool)
+        for t in range(T):
+            pos = np.sort(host(sel["idx"])[t])
+            pos = pos[pos >= 0]
+            assert len(pos) == min(topk, nh[t])
+            kk, vv = R.cache_rows(pl, table_h[t], pos, page, d)
+            qq = host(one[t:t + 1].float())
+            want, z, p = R.attend(qq, kk, vv, d ** -0.5)
+            tol, e = R.attend_tolerance(qq, kk, vv, d ** -0.5, p, "bf16", 2.0 ** -11, 2.0 ** -36)
+            assert np.all(np.abs(host(o[t].float()) - want[0]) <= tol[0])
+            np.add.at(acc_ref[t], pos, p[:, 0].sum(0))
+        assert np.all(np.abs(host(acc) - acc_ref) <= 1e-4 * acc_ref + 1e-6)
+
+    for _ in range(3):
+        step()
+    keep, sink, recent = 200, 4, 16
+    before_k, before_keys = host(pool).copy(), host(keys.float()).copy()
+    idx, n2, acc2 = M.misa_evict_select(acc, n, keep, sink, recent, acc_out=torch.empty_like(acc))
+    acc_h = host(acc)
+    M.misa_kv4_compact(pool, table, idx, d)
+    M.misa_keys_compact_paged(keys, table, idx)
+    after, after_keys = host(pool), host(keys.float())
+    for t in range(T):
+        stay = np.array(R.evict(acc_h[t], int(nh[t]), keep, sink, recent))
+        assert host(idx)[t][:len(stay)].tolist() == stay.tolist()
+        j = np.arange(len(stay))
+        for a, b in zip(R.cache_rows(before_k, table_h[t], stay, page, d), R.cache_rows(after, table_h[t], j, page, d)):
+            assert np.array_equal(a, b)
+        assert np.array_equal(before_keys[table_h[t, stay // page], stay % page], after_keys[table_h[t, j // page], j % page])
+        acc_ref[t] = np.concatenate([acc_ref[t, stay], np.zeros(per * page - len(stay))])
+    n.copy_(n2)
+    nh = host(n2).astype(int)
+    assert nh.tolist() == [200, 200, 200]
+    acc.copy_(acc2)
+    for _ in range(2):
+        step()
+    M.misa_device_check()
