@@ -166,9 +166,10 @@ misa_status misa_device_check(void) {
   const int v = misa::read_and_clear_tc_status();
   const int u = misa::read_and_clear_route_tc_status();
   const int x = misa::read_and_clear_rerank_tc_status();
+  const int y = misa::read_and_clear_prompt_status();
   unsigned int bad[misa::kBadIdKinds];
-  if (v < 0 || u < 0 || x < 0 || !read_bad_ids(bad)) return MISA_ERR_CUDA;
-  if (v || u || x) return MISA_ERR_DEVICE_TIMEOUT;
+  if (v < 0 || u < 0 || x < 0 || y < 0 || !read_bad_ids(bad)) return MISA_ERR_CUDA;
+  if (v || u || x || y) return MISA_ERR_DEVICE_TIMEOUT;
   return (bad[0] || bad[1] || bad[2]) ? MISA_ERR_BAD_INDEX : MISA_OK;
 }
 

@@ -199,8 +199,9 @@ misa_status misa_prompt_attention(const void* q, const void* k, const void* v, i
   if (st == MISA_OK && Tk > 0) st = check_rows(k, ldk, H_kv, d, dtype);
   if (st == MISA_OK && Tk > 0) st = check_rows(v, ldv, H_kv, d, dtype);
   if (st != MISA_OK) return st;
-  misa::launch_prompt_attention(q, k, v, ldq, ldk, ldv, cu_q, cu_k, S, Tq, Tk, H_q, H_kv, d, scale, out, lse_opt,
-                                static_cast<cudaStream_t>(stream));
+  if (!misa::launch_prompt_attention(q, k, v, ldq, ldk, ldv, cu_q, cu_k, S, Tq, Tk, H_q, H_kv, d, scale, out, lse_opt,
+                                     static_cast<cudaStream_t>(stream)))
+    return MISA_ERR_UNSUPPORTED;
   return launch_status();
 }
 

@@ -224,11 +224,13 @@ void launch_evict_select(const float* acc, int64_t ld, const int32_t* n, int T, 
                          int32_t* idx, int32_t* n_out, float* acc_out, int64_t ld_out, cudaStream_t s);
 
 // Causal attention of packed prompts (prompt.cu): q [Tq][Hq][d], k and v [Tk][Hkv][d] at row strides
-// ldq, ldk, ldv; query i of sequence b sees keys j <= i + (keys - queries of b).
-void launch_prompt_attention(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
+// ldq, ldk, ldv; query i of sequence b sees keys j <= i + (keys - queries of b).  False (nothing launched)
+// when the sizes or the missing tensor-map encoder rule it out.
+bool launch_prompt_attention(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
                              const int32_t* cu_q, const int32_t* cu_k, int S, int Tq, int Tk, int Hq, int Hkv, int d,
                              float scale, void* out, float* lse, cudaStream_t s);
 
+int read_and_clear_prompt_status();  // as read_and_clear_tc_status
 bool read_and_clear_bad_ids_kv4_cache(unsigned int* out);
 bool read_and_clear_bad_ids_kv4_attn(unsigned int* out);
 
