@@ -11,7 +11,10 @@
 //   S^T [16 tokens x 8 heads] = K [16 x d] Q^T:   lane (r, c) widens its 16-byte chunk c of rows r, r+8
 //   O^T [d x 8 heads] += V^T [d x 16] P^T:        lane (r, c) widens 8 bytes of tokens 2c, 2c+1, 2c+8, 2c+9,
 //                                                  two tokens' nibbles merged into one byte beforehand
-// e2m1 x e4m3 has 6 significant bits and lies in fp16's range, so the widened K and V are exact in fp16.
+// K enters its product as bare codes, one block of 16 elements a step, and the block's scale multiplies
+// the result in fp32 (both rows of a lane: 4 multiply-adds a step, on twice as many lanes as the 4 fp16
+// multiplications of the operand would have); V's scales run along the contraction and go onto the codes:
+// e2m1 x e4m3 has 6 significant bits and lies in fp16's range, so both operands are exact.
 // The query row is scaled by a power of two into fp16's upper range, where a bf16 row is exact down to
 // 2^-30 of its largest element; an fp32 row is split into two fp16 parts (22 bits), as are its weights.
 // Softmax weights are rounded to fp16 (2^-12) for the product with V where the output is bf16; the sums,
@@ -33,21 +36,21 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;              // tokens of a warp's step
+constexpr int kSub = 16;               // tokens of a product's 16 rows; pages hold whole pieces of 16
+constexpr int kTile = 2 * kSub;        // tokens of a warp's step
 constexpr int kUnit = kWarps * kTile;  // tokens of a CTA's step: the grain of the split
-constexpr int kMaxT = 1024;            // queries per launch
-constexpr int kStages = 4;
+constexpr int kMaxT = 256;             // queries per launch
 constexpr int kMaxCtas = 1024;         // bound on the grid, for workspace sizes that ask no device
 // Weights are kept scaled by 2^kLift against the running maximum, which may lag the true one by
 // 2^kSlack: 2^15 at most, and what fp16 loses at the bottom lies below 2^-35 of the largest weight.
 constexpr float kLift = 11.f, kSlack = 4.f;
-
+// A warp's buffer for one step: two pieces of 16 tokens, each [K codes][V codes][K scales][V scales].
 template <int D>
 struct Stage {
-  static constexpr int kCodes = kTile * D / 2;    // bytes of one side's codes
-  static constexpr int kScales = kTile * D / 16;  // bytes of one side's scales
-  static constexpr int kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kScales, kMask = kVs + kScales;
-  static constexpr int kBytes = kMask + 16;
+  static constexpr int kCodes = kSub * D / 2;    // bytes of one side's codes
+  static constexpr int kScales = kSub * D / 16;  // bytes of one side's scales
+  static constexpr int kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kScales, kPiece = kVs + kScales;
+  static constexpr int kBytes = 2 * kPiece;
 };
 
 struct AttnArgs {
@@ -65,6 +68,7 @@ struct AttnArgs {
   float* part;      // partial results: [slot][8 NT][D] sums, then [slot][8 NT][2] maximum and sum
   float* part_ml;
   uint64_t* pre;    // [T + 1] first unit of each query
+  uint32_t page_mul;  // ceil(2^32 / (page_size / 16)), 0 for pages of 16: logical pages without a division
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -86,9 +90,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-__device__ __forceinline__ uint32_t low2(uint32_t x) { return __byte_perm(x, x, 0x1010); }
-__device__ __forceinline__ uint32_t high2(uint32_t x) { return __byte_perm(x, x, 0x3232); }
-
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -96,19 +97,23 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 
 __device__ __forceinline__ float2 unpack_half2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
-// Copies the first n of BYTES bytes and fills the rest with zeros.
 template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int n) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   if (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Byte i of four e4m3 numbers (not negative) as fp32, times 2^-120.
+__device__ __forceinline__ float scale_bits(uint32_t x, int i) {
+  return __uint_as_float((i < 3 ? x << (20 - 8 * i) : x >> 4) & 0x07f00000u);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -121,6 +126,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ void unit_prefix(const AttnArgs& a, uint64_t* pre, uint64_t* tot) {
   const int per = (a.T + kThreads - 1) / kThreads;
   const int b0 = min(a.T, (int)threadIdx.x * per), b1 = min(a.T, b0 + per);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint64_t local = 0;
   for (int t = b0; t < b1; ++t) {
     const int nt = clamp_len(__ldg(a.n + t), a.L);
@@ -128,27 +134,38 @@ __device__ __forceinline__ void unit_prefix(const AttnArgs& a, uint64_t* pre, ui
     local += (uint64_t)((len + kUnit - 1) / kUnit) * (a.pool.Hkv * a.groups);
     pre[t + 1] = local;
   }
-  tot[threadIdx.x] = local;
+  uint64_t x = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) tot[warp] = x;
   __syncthreads();
-  uint64_t before = 0;
-  for (int i = 0; i < (int)threadIdx.x; ++i) before += tot[i];
+  uint64_t before = x - local;
+  for (int w = 0; w < warp; ++w) before += tot[w];
   for (int t = b0; t < b1; ++t) pre[t + 1] += before;
   if (threadIdx.x == 0) pre[0] = 0;
   __syncthreads();
 }
 
+// CTAs of an SM by registers: 128 a thread hold the state of 8 heads.  (96 and five CTAs also do without
+// spills for bf16, but took 495 us for 480 us at 16 x 128K tokens.)
+__host__ __device__ constexpr int resident_ctas(int HB) { return HB == 16 ? 2 : 4; }
+
 template <int D, int NT, int SPLIT, bool GATHER>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_attn_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, resident_ctas(8 * NT)) kv4_attn_kernel(const AttnArgs a) {
   using St = Stage<D>;
   constexpr int KS = D / 16;      // k-steps of S, and 16-row pieces of O
   constexpr int RB = D / 2;       // bytes of a code row
   constexpr int HB = 8 * NT;      // heads of an item
-  constexpr int kRing = kWarps * kStages * St::kBytes;
+  constexpr int kRing = kWarps * 2 * St::kBytes;
   constexpr int kJoin = kWarps * HB * (D + 2) * 4;
   __shared__ __align__(16) uint8_t ring[kRing > kJoin ? kRing : kJoin];
   __shared__ uint64_t pre[kMaxT + 1];
-  __shared__ uint64_t tot[kThreads];
+  __shared__ uint64_t tot[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  pdl_trigger();
   unit_prefix(a, pre, tot);
   if (blockIdx.x == 0)
     for (int t = threadIdx.x; t <= a.T; t += kThreads) a.pre[t] = pre[t];
@@ -158,8 +175,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_attn_kernel(con
   uint64_t pos = W * blockIdx.x / grid;
   const uint64_t end = W * (blockIdx.x + 1) / grid;
   const int items = a.pool.Hkv * a.groups;
-  const uint32_t my_ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) + warp * kStages * St::kBytes;
-  uint8_t* const my_ptr = ring + warp * kStages * St::kBytes;
+  uint8_t* const my_ptr = ring + warp * 2 * St::kBytes;
+  const uint32_t my_ring = static_cast<uint32_t>(__cvta_generic_to_shared(my_ptr));
+  const int64_t page_bytes = a.pool.page_bytes();
+  const uint32_t slab_bytes = (uint32_t)a.pool.slab_bytes(), scales_at = (uint32_t)a.pool.scales_at();
   int t = 0;
   {
     int hi = a.T - 1;  // last query with pre[t] <= pos
@@ -182,6 +201,88 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_attn_kernel(con
     const int len = GATHER ? a.P : nt;
     const int heads = min(HB, a.G - hg * HB);           // of this item
     const int64_t h0 = (int64_t)t * a.Hq + hk * a.G + hg * HB;
+
+    // warp w takes steps w, w + kWarps, ... of the segment; lane l looks up row l (gathered) or the
+    // first row of its half warp's piece, two steps (gathered: three) before its copy is issued
+    const int p0 = (int)u0 * kUnit + warp * kTile, steps = (int)(u1 - u0);
+    const uint8_t* const slab = a.pool.base + (int64_t)(2 * hk) * slab_bytes;
+    const int32_t* const trow = a.pool.table + (int64_t)t * a.pool.max_pages;
+    const int32_t* const irow = GATHER ? a.idx + (int64_t)t * a.P : nullptr;
+    struct Row {
+      int tok, page, slot;  // tok, page < 0: nothing there
+    };
+    auto token_of = [&](int i) -> int {
+      const int p = p0 + i * kUnit + (GATHER ? lane : (lane & 16));
+      if (i >= steps || p >= len) return -1;
+      if (!GATHER) return p;
+      const int s = __ldg(irow + p);
+      count_bad_id(kBadCandidate, s != -1 && (s < 0 || s >= nt) && item == 0);
+      return s >= 0 && s < nt ? s : -1;
+    };
+    auto row_of = [&](int tok) -> Row {
+      Row w;
+      w.tok = tok;
+      w.page = -1;
+      w.slot = 0;
+      if (tok >= 0) {
+        const uint32_t piece = (uint32_t)tok >> 4;  // of 16 rows; exact below 2^30 rows
+        const uint32_t lp = a.page_mul ? __umulhi(piece, a.page_mul) : piece;
+        w.slot = tok - (int)(lp * (uint32_t)a.pool.page_size);
+        const int pg = __ldg(trow + lp);
+        count_bad_id(kBadPage, (pg < 0 || pg >= a.pool.num_pages) && item == 0 && (GATHER || (lane & 15) == 0));
+        w.page = pg >= 0 && pg < a.pool.num_pages ? pg : -1;
+      }
+      return w;
+    };
+    // starts the copies of one step into buffer st; returns the mask of its rows that are there
+    auto issue = [&](const Row& w, int st) -> uint32_t {
+      const uint32_t dst = my_ring + st * St::kBytes;
+      uint32_t mask;
+      if (!GATHER) {
+        const int l16 = lane & 15;
+        mask = __ballot_sync(0xffffffffu, w.page >= 0 && w.tok + l16 < len);
+        if (w.page >= 0) {
+          const uint32_t d0 = dst + (lane >> 4) * St::kPiece + l16 * 16;
+          const uint8_t* page = slab + w.page * page_bytes;
+          const uint8_t* ks = page + (uint32_t)(w.slot * RB + l16 * 16);
+          const uint8_t* vs = ks + slab_bytes;
+#pragma unroll
+          for (int y = 0; y < St::kCodes / 256; ++y) copy_async<16>(d0 + y * 256, ks + y * 256);
+#pragma unroll
+          for (int y = 0; y < St::kCodes / 256; ++y) copy_async<16>(d0 + St::kV + y * 256, vs + y * 256);
+          constexpr int SC = St::kScales / 16;  // 16-byte pieces of one side's scales
+          if (l16 < 2 * SC)
+            copy_async<16>(d0 + St::kKs, page + (uint32_t)(scales_at + w.slot * KS + (l16 % SC) * 16) + (l16 / SC) * slab_bytes);
+        }
+      } else {
+        mask = __ballot_sync(0xffffffffu, w.page >= 0);
+        const uint8_t* page = slab + (w.page >= 0 ? w.page : 0) * page_bytes;
+        const uint64_t row = reinterpret_cast<uint64_t>(page + (uint32_t)(w.slot * RB));
+        constexpr int CR = RB / 16, RI = 32 / CR;  // 16-byte pieces of a code row, rows a copy covers
+#pragma unroll
+        for (int y = 0; y < kTile / RI; ++y) {
+          const int rw = y * RI + lane / CR;
+          const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, row, rw)) + lane % CR * 16;
+          const uint32_t d0 = dst + (rw >> 4) * St::kPiece + (rw & 15) * RB + lane % CR * 16;
+          if ((mask >> rw) & 1u) {
+            copy_async<16>(d0, src);
+            copy_async<16>(d0 + St::kV, src + slab_bytes);
+          }
+        }
+        if (w.page >= 0) {
+          const uint8_t* sc = page + (uint32_t)(scales_at + w.slot * KS);
+          const uint32_t d0 = dst + (lane >> 4) * St::kPiece + St::kKs + (lane & 15) * KS;
+          copy_async<KS>(d0, sc);
+          copy_async<KS>(d0 + St::kScales, sc + slab_bytes);
+        }
+      }
+      copy_commit();
+      return mask;
+    };
+    Row row_next = row_of(token_of(0));
+    uint32_t mask_next = issue(row_next, 0);
+    row_next = row_of(token_of(1));
+    int tok_next = GATHER ? token_of(2) : 0;
 
     // query fragments: step j, lane (r, c): elements 16 j + 4 c .. + 3 of head r (+ 8)
     uint32_t qf[SPLIT][NT][KS][2];
@@ -244,146 +345,100 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_attn_kernel(con
       for (int i = 0; i < KS; ++i) o[x][i][0] = o[x][i][1] = o[x][i][2] = o[x][i][3] = 0.f;
     }
 
-    // warp w takes tiles w, w + kWarps, ... of the segment
-    const int p0 = (int)u0 * kUnit, tiles = (int)(u1 - u0);
-    const int64_t slab = (int64_t)(2 * hk) * a.pool.slab_bytes();
-    // row lookups run ahead of the copies: the token of tile i + 2 and the page of tile i + 1
-    int tok_next = -1, tok_now = -1;
-    int64_t pg_now = -1;
-    auto token_of = [&](int i) -> int {
-      if (i >= tiles) return -1;
-      const int p = p0 + (i * kWarps + warp) * kTile + (GATHER ? (lane & 15) : 0);
-      if (p >= len) return -1;
-      if (!GATHER) return p;
-      const int s = __ldg(a.idx + (int64_t)t * a.P + p);
-      count_bad_id(kBadCandidate, s != -1 && (s < 0 || s >= nt) && lane < 16 && item == 0);
-      return s >= 0 && s < nt ? s : -1;
-    };
-    auto page_of = [&](int tok) -> int64_t {
-      return kv4_page(a.pool, t, tok, item == 0 && (GATHER ? lane < 16 : lane == 0));
-    };
-    // copies tile i into stage st; tok and pg are its first token (gathered: of row lane & 15) and page
-    auto issue = [&](int i, int st, int tok, int64_t pg) {
-      if (i < tiles) {
-        const uint32_t dst = my_ring + st * St::kBytes;
-        const int sl = tok < 0 ? 0 : (int)((uint32_t)tok % (uint32_t)a.pool.page_size);
-        if (!GATHER) {
-          const int rows = pg < 0 ? 0 : min(kTile, len - tok);
-          const uint8_t* base = a.pool.base + (pg < 0 ? 0 : pg * a.pool.page_bytes()) + slab;
-#pragma unroll
-          for (int side = 0; side < 2; ++side) {
-            const uint8_t* src = base + side * a.pool.slab_bytes() + (int64_t)sl * RB;
-#pragma unroll
-            for (int y = lane; y < St::kCodes / 16; y += 32)
-              copy_async<16>(dst + side * St::kV + y * 16, src + y * 16, y * 16 / RB < rows ? 16 : 0);
-          }
-          constexpr int SC = St::kScales / 16;  // 16-byte pieces of one side's scales
-          if (lane < 2 * SC) {
-            const int side = lane / SC, y = lane % SC;
-            copy_async<16>(dst + St::kKs + side * St::kScales + y * 16,
-                           base + side * a.pool.slab_bytes() + a.pool.scales_at() + (int64_t)sl * KS + y * 16,
-                           max(0, min(16, rows * KS - y * 16)));  // rows past the prefix: zero scales
-          }
-          if (lane == 0)
-            *reinterpret_cast<uint32_t*>(my_ptr + st * St::kBytes + St::kMask) = (1u << rows) - 1u;
-        } else {
-          const bool there = pg >= 0;
-          const uint32_t mask = __ballot_sync(0xffffffffu, there) & 0xffffu;
-          const int64_t row = there ? pg * a.pool.page_bytes() + slab : 0;
-          constexpr int CR = RB / 16;  // 16-byte pieces of a code row
-#pragma unroll
-          for (int y = 0; y < kTile * CR / 32; ++y) {
-            const int at_row = (y * 32 + lane) / CR, piece = (y * 32 + lane) % CR;
-            const int64_t b = __shfl_sync(0xffffffffu, row, at_row);
-            const int s1 = __shfl_sync(0xffffffffu, sl, at_row);
-            const uint8_t* src = a.pool.base + b + (int64_t)s1 * RB + piece * 16;
-            const bool ok = (mask >> at_row) & 1u;
-            copy_async<16>(dst + at_row * RB + piece * 16, src, ok ? 16 : 0);
-            copy_async<16>(dst + St::kV + at_row * RB + piece * 16, ok ? src + a.pool.slab_bytes() : src, ok ? 16 : 0);
-          }
-          const int side = lane >> 4;
-          copy_async<KS>(dst + St::kKs + side * St::kScales + (lane & 15) * KS,
-                         a.pool.base + row + side * a.pool.slab_bytes() + a.pool.scales_at() + (int64_t)sl * KS,
-                         there ? KS : 0);
-          if (lane == 0) *reinterpret_cast<uint32_t*>(my_ptr + st * St::kBytes + St::kMask) = mask;
-        }
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+      const uint32_t mask = mask_next;
+      copy_wait<0>();
+      __syncwarp();  // the step's rows are in, and the other buffer's have been used by every lane
+      if (i + 1 < steps) {
+        mask_next = issue(row_next, (i + 1) & 1);
+        row_next = row_of(GATHER ? tok_next : token_of(i + 2));
+        if (GATHER) tok_next = token_of(i + 3);
       }
-      copy_commit();
-    };
-    tok_now = token_of(0);
-    tok_next = token_of(1);
-    pg_now = page_of(tok_now);
-    auto advance = [&](int i, int st) {  // issues tile i; its token and page are in the *_now values
-      issue(i, st, tok_now, pg_now);
-      tok_now = tok_next;
-      pg_now = page_of(tok_now);
-      tok_next = token_of(i + 2);
-    };
-#pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) advance(i, i);
-
-#pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-      const int st = i % kStages;
-      copy_wait<kStages - 2>();
-      __syncwarp();
-      advance(i + kStages - 1, (i + kStages - 1) % kStages);
-      const uint8_t* sp = my_ptr + st * St::kBytes;
-      const uint32_t mask = *reinterpret_cast<const uint32_t*>(sp + St::kMask);
+      uint8_t* sp = my_ptr + (i & 1) * St::kBytes;
+      if (mask != 0xffffffffu) {
+        // rows that are not there hold what the buffer held before: any codes are numbers, scales of zero
+        // make them zeros
+        if (!((mask >> lane) & 1u)) {
+          uint8_t* z = sp + (lane >> 4) * St::kPiece + St::kKs + (lane & 15) * KS;
+#pragma unroll
+          for (int y = 0; y < KS / 4; ++y)
+            *reinterpret_cast<uint32_t*>(z + 4 * y) = *reinterpret_cast<uint32_t*>(z + St::kScales + 4 * y) = 0u;
+        }
+        __syncwarp();
+      }
 
       // S^T = K Q^T
-      float s[NT][4];
+      float s[2][NT][4];
 #pragma unroll
-      for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
-      uint32_t ka[KS / 2], kb[KS / 2], sa[KS / 4], sb[KS / 4];
-      if constexpr (D == 128) {
-        const uint4 u = *reinterpret_cast<const uint4*>(sp + r * RB + c * 16);
-        const uint4 v = *reinterpret_cast<const uint4*>(sp + (r + 8) * RB + c * 16);
-        ka[0] = u.x, ka[1] = u.y, ka[2] = u.z, ka[3] = u.w;
-        kb[0] = v.x, kb[1] = v.y, kb[2] = v.z, kb[3] = v.w;
-        const uint2 e = *reinterpret_cast<const uint2*>(sp + St::kKs + r * KS);
-        const uint2 f = *reinterpret_cast<const uint2*>(sp + St::kKs + (r + 8) * KS);
-        sa[0] = e.x, sa[1] = e.y, sb[0] = f.x, sb[1] = f.y;
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(sp + r * RB + c * 8);
-        const uint2 v = *reinterpret_cast<const uint2*>(sp + (r + 8) * RB + c * 8);
-        ka[0] = u.x, ka[1] = u.y;
-        kb[0] = v.x, kb[1] = v.y;
-        sa[0] = *reinterpret_cast<const uint32_t*>(sp + St::kKs + r * KS);
-        sb[0] = *reinterpret_cast<const uint32_t*>(sp + St::kKs + (r + 8) * KS);
-      }
+      for (int g = 0; g < 2; ++g) {
+        const uint8_t* kp = sp + g * St::kPiece;
 #pragma unroll
-      for (int w = 0; w < KS / 2; ++w) {
-        uint32_t x0[4], x1[4];
-        e2m1x8_to_half2(ka[w], x0[0], x0[1], x0[2], x0[3]);
-        e2m1x8_to_half2(kb[w], x1[0], x1[1], x1[2], x1[3]);
-        const uint32_t e = e4m3x2_to_half2((uint16_t)(sa[w / 2] >> (16 * (w & 1))));
-        const uint32_t f = e4m3x2_to_half2((uint16_t)(sb[w / 2] >> (16 * (w & 1))));
+        for (int x = 0; x < NT; ++x) s[g][x][0] = s[g][x][1] = s[g][x][2] = s[g][x][3] = 0.f;
+        uint32_t ka[KS / 2], kb[KS / 2], sa[KS / 4], sb[KS / 4];
+        if constexpr (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(kp + r * RB + c * 16);
+          const uint4 v = *reinterpret_cast<const uint4*>(kp + (r + 8) * RB + c * 16);
+          ka[0] = u.x, ka[1] = u.y, ka[2] = u.z, ka[3] = u.w;
+          kb[0] = v.x, kb[1] = v.y, kb[2] = v.z, kb[3] = v.w;
+          const uint2 e = *reinterpret_cast<const uint2*>(kp + St::kKs + r * KS);
+          const uint2 f = *reinterpret_cast<const uint2*>(kp + St::kKs + (r + 8) * KS);
+          sa[0] = e.x, sa[1] = e.y, sb[0] = f.x, sb[1] = f.y;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(kp + r * RB + c * 8);
+          const uint2 v = *reinterpret_cast<const uint2*>(kp + (r + 8) * RB + c * 8);
+          ka[0] = u.x, ka[1] = u.y;
+          kb[0] = v.x, kb[1] = v.y;
+          sa[0] = *reinterpret_cast<const uint32_t*>(kp + St::kKs + r * KS);
+          sb[0] = *reinterpret_cast<const uint32_t*>(kp + St::kKs + (r + 8) * KS);
+        }
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const uint32_t ee = y ? high2(e) : low2(e), ff = y ? high2(f) : low2(f);
-          const uint32_t a0 = hmul2(x0[2 * y], ee), a1 = hmul2(x1[2 * y], ff), a2 = hmul2(x0[2 * y + 1], ee),
-                         a3 = hmul2(x1[2 * y + 1], ff);
+        for (int w = 0; w < KS / 2; ++w) {
+          uint32_t x0[4], x1[4];
+          e2m1x8_to_half2(ka[w], x0[0], x0[1], x0[2], x0[3]);
+          e2m1x8_to_half2(kb[w], x1[0], x1[1], x1[2], x1[3]);
 #pragma unroll
-          for (int x = 0; x < NT; ++x)
+          for (int y = 0; y < 2; ++y) {
+            // a block's products come out unscaled; its scale of either row goes on in fp32, as the e4m3
+            // number times 2^-120 (its bits at the bottom of the exponent field; also below e4m3's normal range)
+            const float ea = scale_bits(sa[w / 2], (2 * w + y) % 4), eb = scale_bits(sb[w / 2], (2 * w + y) % 4);
 #pragma unroll
-            for (int z = 0; z < SPLIT; ++z)
-              mma_f16(s[x], a0, a1, a2, a3, qf[z][x][2 * w + y][0], qf[z][x][2 * w + y][1]);
+            for (int x = 0; x < NT; ++x) {
+              float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int z = 0; z < SPLIT; ++z)
+                mma_f16(d, x0[2 * y], x1[2 * y], x0[2 * y + 1], x1[2 * y + 1], qf[z][x][2 * w + y][0],
+                        qf[z][x][2 * w + y][1]);
+              s[g][x][0] = fmaf(ea, d[0], s[g][x][0]);
+              s[g][x][1] = fmaf(ea, d[1], s[g][x][1]);
+              s[g][x][2] = fmaf(eb, d[2], s[g][x][2]);
+              s[g][x][3] = fmaf(eb, d[3], s[g][x][3]);
+            }
+          }
         }
       }
-      // logits in base 2, rows without a token minus infinity; s[x][0..1] row r, s[x][2..3] row r + 8
-      const bool v0 = (mask >> r) & 1u, v1 = (mask >> (r + 8)) & 1u;
-      bool raise = false;
+      // logits in base 2, rows without a token minus infinity; s[g][x][0..1] row r, s[g][x][2..3] row r + 8
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        s[x][0] = v0 ? s[x][0] * mul[x][0] : -INFINITY;
-        s[x][1] = v0 ? s[x][1] * mul[x][1] : -INFINITY;
-        s[x][2] = v1 ? s[x][2] * mul[x][0] : -INFINITY;
-        s[x][3] = v1 ? s[x][3] * mul[x][1] : -INFINITY;
-        raise |= fmaxf(s[x][0], s[x][2]) > m[x][0] + kSlack || fmaxf(s[x][1], s[x][3]) > m[x][1] + kSlack;
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) s[g][x][y] = s[g][x][y] * 0x1p120f * mul[x][y & 1];
+      if (mask != 0xffffffffu) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const bool v0 = (mask >> (16 * g + r)) & 1u, v1 = (mask >> (16 * g + r + 8)) & 1u;
+#pragma unroll
+          for (int x = 0; x < NT; ++x) {
+            s[g][x][0] = v0 ? s[g][x][0] : -INFINITY;
+            s[g][x][1] = v0 ? s[g][x][1] : -INFINITY;
+            s[g][x][2] = v1 ? s[g][x][2] : -INFINITY;
+            s[g][x][3] = v1 ? s[g][x][3] : -INFINITY;
+          }
+        }
       }
       if (a.logits) {
-        const int p = p0 + (i * kWarps + warp) * kTile + r;
+        const int p = p0 + i * kUnit + r;
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -391,22 +446,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_attn_kernel(con
             const int head = x * 8 + 2 * c + y;
             if (head < heads) {
               float* row = a.logits + (h0 + head) * a.ldS + p;
-              row[0] = s[x][y];
-              row[8] = s[x][2 + y];
+              row[0] = s[0][x][y];
+              row[8] = s[0][x][2 + y];
+              row[16] = s[1][x][y];
+              row[24] = s[1][x][2 + y];
             }
           }
       }
       // the running maximum is raised only when a logit passes it by kSlack
+      float top[NT][2];
+      bool raise = false;
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          top[x][y] = fmaxf(fmaxf(s[0][x][y], s[0][x][2 + y]), fmaxf(s[1][x][y], s[1][x][2 + y]));
+          raise |= top[x][y] > m[x][y] + kSlack;
+        }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            float top = fmaxf(s[x][y], s[x][2 + y]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float next = fmaxf(m[x][y], top);
+            float v = top[x][y];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            const float next = fmaxf(m[x][y], v);
             const float f = m[x][y] == next ? 1.f : exp2_fast(m[x][y] - next);
             m[x][y] = next;
             l[x][y] *= f;
@@ -417,54 +483,72 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_attn_kernel(con
             }
           }
       }
-      uint32_t pb[SPLIT][NT][2];
+      uint32_t pb[2][SPLIT][NT][2];
 #pragma unroll
       for (int x = 0; x < NT; ++x) {
         const float z0 = m[x][0] == -INFINITY ? 0.f : m[x][0] - kLift, z1 = m[x][1] == -INFINITY ? 0.f : m[x][1] - kLift;
-        const float w0 = exp2_fast(s[x][0] - z0), w1 = exp2_fast(s[x][1] - z1);
-        const float w2 = exp2_fast(s[x][2] - z0), w3 = exp2_fast(s[x][3] - z1);
-        l[x][0] += w0 + w2;
-        l[x][1] += w1 + w3;
-        const uint32_t h0_ = pack_half2(w0, w1), h1_ = pack_half2(w2, w3);
-        pb[0][x][0] = transpose8(h0_);
-        pb[0][x][1] = transpose8(h1_);
-        if (SPLIT == 2) {
-          const float2 b0 = unpack_half2(h0_), b1 = unpack_half2(h1_);
-          pb[SPLIT - 1][x][0] = transpose8(pack_half2(w0 - b0.x, w1 - b0.y));
-          pb[SPLIT - 1][x][1] = transpose8(pack_half2(w2 - b1.x, w3 - b1.y));
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float w0 = exp2_fast(s[g][x][0] - z0), w1 = exp2_fast(s[g][x][1] - z1);
+          const float w2 = exp2_fast(s[g][x][2] - z0), w3 = exp2_fast(s[g][x][3] - z1);
+          l[x][0] += w0 + w2;
+          l[x][1] += w1 + w3;
+          const uint32_t h0_ = pack_half2(w0, w1), h1_ = pack_half2(w2, w3);
+          pb[g][0][x][0] = transpose8(h0_);
+          pb[g][0][x][1] = transpose8(h1_);
+          if (SPLIT == 2) {
+            const float2 b0 = unpack_half2(h0_), b1 = unpack_half2(h1_);
+            pb[g][SPLIT - 1][x][0] = transpose8(pack_half2(w0 - b0.x, w1 - b0.y));
+            pb[g][SPLIT - 1][x][1] = transpose8(pack_half2(w2 - b1.x, w3 - b1.y));
+          }
         }
       }
 
       // O^T += V^T P^T: byte i of a lane's chunk holds piece i's rows r (low nibble) and r + 8 (high)
-      const uint8_t* vp = sp + St::kV + r * (RB / 8);
-      const uint8_t* vs = sp + St::kVs + (r & 1) * (KS / 2);
 #pragma unroll
-      for (int w = 0; w < KS / 4; ++w) {  // 4 pieces, 2 blocks of 16 elements
-        uint32_t lo[2][4], hi[2][4];
+      for (int g = 0; g < 2; ++g) {
+        constexpr int W = KS / 4;  // words of a lane's chunk: 4 pieces, 2 blocks of 16 elements each
+        const uint8_t* vp = sp + g * St::kPiece + St::kV + r * (RB / 8);
+        const uint8_t* vs = sp + g * St::kPiece + St::kVs + (r & 1) * (KS / 2);
+        uint32_t xv[4][W], ev[4];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {  // tokens 2c, 2c + 1, then 8 further
-          const int ta = 2 * c + 8 * hf;
-          const uint32_t xa = *reinterpret_cast<const uint32_t*>(vp + ta * RB + 4 * w);
-          const uint32_t xb = *reinterpret_cast<const uint32_t*>(vp + (ta + 1) * RB + 4 * w);
-          e2m1x8_to_half2((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), lo[hf][0], lo[hf][1], lo[hf][2], lo[hf][3]);
-          e2m1x8_to_half2(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), hi[hf][0], hi[hf][1], hi[hf][2], hi[hf][3]);
-          const uint32_t ea = *reinterpret_cast<const uint16_t*>(vs + ta * KS + 2 * w);
-          const uint32_t eb = *reinterpret_cast<const uint16_t*>(vs + (ta + 1) * KS + 2 * w);
-          const uint32_t ab = __byte_perm(ea, eb, 0x5140);  // scales of block 0: a, b; of block 1: a, b
-          const uint32_t f0 = e4m3x2_to_half2((uint16_t)ab), f1 = e4m3x2_to_half2((uint16_t)(ab >> 16));
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            lo[hf][y] = hmul2(lo[hf][y], y < 2 ? f0 : f1);
-            hi[hf][y] = hmul2(hi[hf][y], y < 2 ? f0 : f1);
+        for (int y = 0; y < 4; ++y) {
+          const int tk = 2 * c + (y & 1) + 8 * (y >> 1);
+          if constexpr (D == 128) {
+            const uint2 u = *reinterpret_cast<const uint2*>(vp + tk * RB);
+            xv[y][0] = u.x;
+            xv[y][W - 1] = u.y;
+            ev[y] = *reinterpret_cast<const uint32_t*>(vs + tk * KS);
+          } else {
+            xv[y][0] = *reinterpret_cast<const uint32_t*>(vp + tk * RB);
+            ev[y] = *reinterpret_cast<const uint16_t*>(vs + tk * KS);
           }
         }
 #pragma unroll
-        for (int y = 0; y < 4; ++y)
+        for (int w = 0; w < W; ++w) {
+          uint32_t lo[2][4], hi[2][4];
 #pragma unroll
-          for (int x = 0; x < NT; ++x)
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t xa = xv[2 * hf][w], xb = xv[2 * hf + 1][w];
+            e2m1x8_to_half2((xa & 0x0f0f0f0fu) | ((xb << 4) & 0xf0f0f0f0u), lo[hf][0], lo[hf][1], lo[hf][2], lo[hf][3]);
+            e2m1x8_to_half2(((xa >> 4) & 0x0f0f0f0fu) | (xb & 0xf0f0f0f0u), hi[hf][0], hi[hf][1], hi[hf][2], hi[hf][3]);
+            // scales of the word's first block: a, b; of its second: a, b
+            const uint32_t ab = __byte_perm(ev[2 * hf], ev[2 * hf + 1], w ? 0x7362 : 0x5140);
+            const uint32_t f0 = e4m3x2_to_half2((uint16_t)ab), f1 = e4m3x2_to_half2((uint16_t)(ab >> 16));
 #pragma unroll
-            for (int z = 0; z < SPLIT; ++z)
-              mma_f16(o[x][4 * w + y], lo[0][y], hi[0][y], lo[1][y], hi[1][y], pb[z][x][0], pb[z][x][1]);
+            for (int y = 0; y < 4; ++y) {
+              lo[hf][y] = hmul2(lo[hf][y], y < 2 ? f0 : f1);
+              hi[hf][y] = hmul2(hi[hf][y], y < 2 ? f0 : f1);
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+              for (int z = 0; z < SPLIT; ++z)
+                mma_f16(o[x][4 * w + y], lo[0][y], hi[0][y], lo[1][y], hi[1][y], pb[g][z][x][0], pb[g][z][x][1]);
+        }
       }
     }
     copy_wait<0>();
@@ -543,52 +627,87 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 4 : 2) kv4_attn_kernel(con
   }
 }
 
-// Joins the pieces of every (query, head) whose tokens more than one CTA took; also writes the heads
-// of queries that attend to nothing.  One warp per head.
+// Joins the pieces of a (query, head) whose tokens more than one CTA took; also writes the heads of
+// queries that attend to nothing.  One CTA per head: its threads first weigh the pieces (each by its
+// maximum against the largest), then its warps add up every eighth piece.
 template <int D, int SPLIT>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a, int HB, int64_t ctas) {
+  constexpr int E = D / 32;  // output elements of a lane
+  __shared__ float weight[kMaxCtas];
+  __shared__ float red[8];
+  __shared__ __align__(16) float part[8][D];
   pdl_wait();
-  const int64_t hd = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (hd >= (int64_t)a.T * a.Hq) return;
-  const int t = (int)(hd / a.Hq), hq = (int)(hd % a.Hq);
+  const int hd = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = hd / a.Hq, hq = hd % a.Hq;
   const int hk = hq / a.G, hr = hq % a.G, head = hr % HB;
   const int items = a.pool.Hkv * a.groups, item = hk * a.groups + hr / HB;
   const uint64_t W = a.pre[a.T], first = a.pre[t];
   const uint64_t units = (a.pre[t + 1] - first) / items;
-  constexpr int E = D / 32;  // output elements of a lane
-  float acc[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float top = -INFINITY, sum = 0.f;
+  int pieces = 0;
+  int64_t slot0 = 0;
   if (units > 0) {
     const uint64_t grid = W < (uint64_t)ctas ? W : (uint64_t)ctas;
     const uint64_t p0 = first + item * units, p1 = p0 + units;
     const int64_t c0 = (int64_t)(((p0 + 1) * grid - 1) / W), c1 = (int64_t)((p1 * grid - 1) / W);
     if (c0 == c1) return;  // one CTA had the whole head
-    const int64_t slot0 = c0 + (int64_t)t * items + item;
-    const int pieces = (int)(c1 - c0 + 1);
-    for (int i = lane; i < pieces; i += 32) top = fmaxf(top, a.part_ml[((slot0 + i) * HB + head) * 2]);
+    slot0 = c0 + (int64_t)t * items + item;
+    pieces = (int)(c1 - c0 + 1);
+  }
+  auto over_block = [&](float v, bool largest) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-      const int64_t at = (slot0 + i) * HB + head;
-      const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-      const float* p = a.part + at * D + lane * E;
-      const float f = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);
-      sum += f * ml.y;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += f * p[e];
+    for (int o = 16; o; o >>= 1) {
+      const float w = __shfl_xor_sync(0xffffffffu, v, o);
+      v = largest ? fmaxf(v, w) : v + w;
     }
-  }
-  const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+    __syncthreads();
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = red[0];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if (SPLIT == 1) static_cast<__nv_bfloat16*>(a.out)[hd * D + lane * E + e] = __float2bfloat16_rn(acc[e] * inv);
-    else static_cast<float*>(a.out)[hd * D + lane * E + e] = acc[e] * inv;
+    for (int w = 1; w < 8; ++w) v = largest ? fmaxf(v, red[w]) : v + red[w];
+    return v;
+  };
+  constexpr int kPer = kMaxCtas / 256;
+  float2 ml[kPer];
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int i = x * 256 + threadIdx.x;
+    ml[x] = i < pieces ? *reinterpret_cast<const float2*>(a.part_ml + ((slot0 + i) * HB + head) * 2) : make_float2(-INFINITY, 0.f);
+    top = fmaxf(top, ml[x].x);
   }
-  if (lane == 0) {
+  top = over_block(top, true);
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int i = x * 256 + threadIdx.x;
+    const float f = ml[x].y == 0.f ? 0.f : exp2_fast(ml[x].x - top);
+    if (i < pieces) weight[i] = f;
+    sum += f * ml[x].y;
+  }
+  sum = over_block(sum, false);
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < pieces; i += 8) {
+    const float* p = a.part + ((slot0 + i) * HB + head) * D + lane * E;
+    const float f = weight[i];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += f * p[e];
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += part[w][threadIdx.x];
+    v *= sum == 0.f ? 0.f : a.v_scale / sum;
+    const int64_t at = (int64_t)hd * D + threadIdx.x;
+    if (SPLIT == 1) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+    else static_cast<float*>(a.out)[at] = v;
+  }
+  if (threadIdx.x == 0) {
     const float z = sum == 0.f ? -INFINITY : top + log2f(sum) - kLift;
     if (a.lse) a.lse[hd] = z * 0.693147180559945309f;
     if (a.lse2) a.lse2[hd] = z;
@@ -625,7 +744,7 @@ int heads_per_item(int G) { return G > 8 ? 16 : 8; }
 int64_t attn_ctas(int T, int P, int Hkv, int G) {
   const int HB = heads_per_item(G);
   const int64_t most = (int64_t)T * Hkv * ((G + HB - 1) / HB) * ((P + kUnit - 1) / kUnit);
-  const int64_t full = std::min<int64_t>((int64_t)sm_count() * (HB == 8 ? 4 : 2), kMaxCtas);
+  const int64_t full = std::min<int64_t>((int64_t)sm_count() * resident_ctas(HB), kMaxCtas);
   return std::min(most, full);
 }
 
@@ -637,8 +756,7 @@ void launch_attn(const AttnArgs& a, float* acc, int64_t ld_acc, int64_t ctas, cu
     if (a.idx) kv4_attn_kernel<D, NT, SPLIT, true><<<(unsigned)ctas, kThreads, 0, s>>>(a);
     else kv4_attn_kernel<D, NT, SPLIT, false><<<(unsigned)ctas, kThreads, 0, s>>>(a);
   }
-  const int64_t hd = (int64_t)a.T * a.Hq;
-  launch_pdl(kv4_join_kernel<D, SPLIT>, dim3((unsigned)((hd + 7) / 8)), dim3(256), 0, s, a, 8 * NT, ctas);
+  launch_pdl(kv4_join_kernel<D, SPLIT>, dim3((unsigned)(a.T * a.Hq)), dim3(256), 0, s, a, 8 * NT, ctas);
   if (acc) launch_pdl(kv4_weights_kernel, dim3((a.P + 255) / 256, a.T), dim3(256), 0, s, a, acc, ld_acc);
 }
 
@@ -649,7 +767,7 @@ size_t kv4_attention_ws_bytes(int T, int P, int Hq, int Hkv, int d, bool weights
   const int Tc = T < kMaxT ? T : kMaxT;
   const int64_t slots = kMaxCtas + (int64_t)Tc * Hkv * ((G + HB - 1) / HB);
   size_t b = up256(sizeof(uint64_t) * (kMaxT + 1)) + up256(sizeof(float) * slots * HB * d) + up256(sizeof(float) * slots * HB * 2);
-  if (weights) b += up256(sizeof(float) * (size_t)Tc * Hq) + up256(sizeof(float) * (size_t)Tc * Hq * ((P + 63) / 64 * 64));
+  if (weights) b += up256(sizeof(float) * (size_t)Tc * Hq) + up256(sizeof(float) * (size_t)Tc * Hq * (((size_t)P + kUnit - 1) / kUnit * kUnit));
   return b;
 }
 
@@ -674,6 +792,8 @@ void launch_kv4_attention(DType dt, const void* q, const Kv4Pool& pool, const in
     a.groups = (G + HB - 1) / HB;
     a.scale = scale * k_scale * 1.44269504088896341f;
     a.v_scale = v_scale;
+    const uint32_t pieces = (uint32_t)pool.page_size / kSub;
+    a.page_mul = pieces == 1 ? 0u : (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
     a.out = static_cast<char*>(out) + elt * t0 * (size_t)Hq * pool.d;
     a.lse = lse ? lse + (int64_t)t0 * Hq : nullptr;
     const int64_t ctas = attn_ctas(Tc, a.P, pool.Hkv, G);
@@ -693,7 +813,7 @@ void launch_kv4_attention(DType dt, const void* q, const Kv4Pool& pool, const in
       a.lse2 = reinterpret_cast<float*>(p);
       p += up256(sizeof(float) * (size_t)Tc * Hq);
       a.logits = reinterpret_cast<float*>(p);
-      a.ldS = (a.P + 63) / 64 * 64;
+      a.ldS = (a.P + kUnit - 1) / kUnit * (int64_t)kUnit;
       ac = acc + (int64_t)t0 * ld_acc;
     }
     const bool f32 = dt == DType::F32;
