@@ -349,7 +349,7 @@ misa_status misa_hier_topk_fused(const void* q, const float* w, const void* k, i
  * (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign) times it:
  *   s_b = e4m3(max |x_i| / (6 g)),  code_i = e2m1(x_i / (s_b g)),  and x_i reads as code_i s_b g
  * over the 16 elements i of block b, both conversions to nearest with ties to even, the divisions and
- * 6 g in fp32; g is k_scale or v_scale, one positive fp32 number per tensor (1 suits blocks whose
+ * 6 g in fp32; g is k_scale or v_scale, one fp32 number in [2^-60, 2^60] per tensor (1 suits blocks whose
  * largest element lies between about 0.1 and 2688; larger elements saturate, NaN stores as 0, infinite
  * elements as the largest value).  A block whose scale rounds to 0 stores zeros.
  *   pool       : uint8 [num_pages][H_kv][2][page_size * 9 d / 16], 16-byte aligned; the slab of one
@@ -422,6 +422,7 @@ misa_status misa_evict_select(const float* acc, int64_t ld_acc, const int32_t* n
  * T sequences must be theirs alone.
  *   ws : misa_workspace_bytes(MISA_OP_KV4_COMPACT, T, 0, H_kv, 0, d, keep, 0), and
  *        misa_workspace_bytes(MISA_OP_KEYS_COMPACT_PAGED, T, 0, 0, 0, bytes of a key row, keep, 0) bytes
+ *        (marks of which rows have been read; cleared by the call)
  */
 misa_status misa_kv4_compact(void* pool, int64_t num_pages, int page_size, const int32_t* page_table,
                              int64_t max_pages, const int32_t* idx, int T, int keep, int H_kv, int d, void* ws,

@@ -31,8 +31,8 @@ LIB_PATH = os.path.join(PKG, "libmisa_checked.so" if os.environ.get("MISA_LIBRAR
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOUT, ERR_BAD_INDEX = range(7)
 BF16, F32 = 0, 1
 (OP_ROUTE, OP_SCORE_TOPK, OP_RERANK, OP_DENSE_TOPK, OP_TOPK_SELECT, OP_BLOCK_FILTER, OP_ROUTE_PAGED,
- OP_SCORE_TOPK_PAGED, OP_RERANK_PAGED, OP_SCORE_TOPK_FUSED, OP_HIER_FUSED, OP_KV4_ATTENTION, OP_KV4_COMPACT,
- OP_KEYS_COMPACT_PAGED) = range(14)
+ OP_SCORE_TOPK_PAGED, OP_RERANK_PAGED, OP_SCORE_TOPK_FUSED, OP_HIER_FUSED,
+ OP_KV4_ATTENTION, OP_KV4_COMPACT, OP_KEYS_COMPACT_PAGED) = range(14)
 MAX_KP = 16384
 
 if not os.path.exists(LIB_PATH):

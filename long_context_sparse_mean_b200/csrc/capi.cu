@@ -167,9 +167,10 @@ misa_status misa_device_check(void) {
   const int u = misa::read_and_clear_route_tc_status();
   const int x = misa::read_and_clear_rerank_tc_status();
   const int y = misa::read_and_clear_prompt_status();
+  const int z = misa::read_and_clear_compact_status();
   unsigned int bad[misa::kBadIdKinds];
-  if (v < 0 || u < 0 || x < 0 || y < 0 || !read_bad_ids(bad)) return MISA_ERR_CUDA;
-  if (v || u || x || y) return MISA_ERR_DEVICE_TIMEOUT;
+  if (v < 0 || u < 0 || x < 0 || y < 0 || z < 0 || !read_bad_ids(bad)) return MISA_ERR_CUDA;
+  if (v || u || x || y || z) return MISA_ERR_DEVICE_TIMEOUT;
   return (bad[0] || bad[1] || bad[2]) ? MISA_ERR_BAD_INDEX : MISA_OK;
 }
 
@@ -210,9 +211,9 @@ size_t misa_workspace_bytes(int op, int T, int L, int H_I, int B, int h, int top
       if (T <= 0 || L <= 0 || H_I <= 0 || B <= 0 || H_I % B != 0 || h <= 0) return 0;
       return misa::kv4_attention_ws_bytes(T, topk > 0 ? topk : L, H_I, B, h, kp != 0);
     case MISA_OP_KV4_COMPACT:  // H_I kv heads, h head width, topk kept tokens
-      return T > 0 && H_I > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, (int64_t)H_I * 2 * (9 * h / 16)) : 0;
+      return T > 0 && H_I > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, 2 * H_I, h / 2, h / 16) : 0;
     case MISA_OP_KEYS_COMPACT_PAGED:  // h bytes of a key row, topk kept tokens
-      return T > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, h) : 0;
+      return T > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, 1, h, 0) : 0;
     default:
       return 0;
   }

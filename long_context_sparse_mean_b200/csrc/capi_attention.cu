@@ -49,6 +49,9 @@ Kv4Pool to_pool(const void* pool, int64_t num_pages, int page_size, const int32_
 
 bool positive(float x) { return x > 0.f && std::isfinite(x); }
 
+// A cache's factor: far enough from the ends of fp32's range for a block's scale times it and its inverse.
+bool factor(float x) { return x >= 0x1p-60f && x <= 0x1p60f; }
+
 // Packed rows [rows][H][d] at stride ld elements that are read or written in 16-byte pieces.
 misa_status check_rows(const void* p, int64_t ld, int H, int d, int dtype) {
   const int piece = dtype == MISA_F32 ? 4 : 8;
@@ -68,7 +71,7 @@ misa_status misa_kv4_append(const void* k, const void* v, int64_t ldk, int64_t l
   if (dtype != MISA_BF16 && dtype != MISA_F32) return MISA_ERR_UNSUPPORTED;
   misa_status st = check_kv4(num_pages, page_size, max_pages, H_kv, d);
   if (st != MISA_OK) return st;
-  if (!positive(k_scale) || !positive(v_scale)) return MISA_ERR_INVALID_ARG;
+  if (!factor(k_scale) || !factor(v_scale)) return MISA_ERR_INVALID_ARG;
   if ((int64_t)rows * H_kv > INT32_MAX) return MISA_ERR_UNSUPPORTED;
   if (S == 0 || rows == 0) return MISA_OK;
   if (!pool || !at16(pool) || !page_table || !cu || !start) return MISA_ERR_INVALID_ARG;
@@ -88,7 +91,7 @@ misa_status misa_kv4_read(const void* pool, int64_t num_pages, int page_size, co
   if (dtype != MISA_BF16 && dtype != MISA_F32) return MISA_ERR_UNSUPPORTED;
   const misa_status st = check_kv4(num_pages, page_size, max_pages, H_kv, d);
   if (st != MISA_OK) return st;
-  if (!positive(k_scale) || !positive(v_scale)) return MISA_ERR_INVALID_ARG;
+  if (!factor(k_scale) || !factor(v_scale)) return MISA_ERR_INVALID_ARG;
   if ((int64_t)rows * H_kv > INT32_MAX) return MISA_ERR_UNSUPPORTED;
   if (S == 0 || rows == 0) return MISA_OK;
   if (!pool || !at16(pool) || !page_table || !cu || !start || !k || !v || !at16(k) || !at16(v))
@@ -109,7 +112,7 @@ misa_status misa_kv4_attention(const void* q, const void* pool, int64_t num_page
   if (st != MISA_OK) return st;
   if (H_q % H_kv != 0 || (int64_t)L > max_pages * page_size) return MISA_ERR_INVALID_ARG;
   if (L > kMaxLen || (idx && P > kMaxLen) || H_q > 65536) return MISA_ERR_UNSUPPORTED;
-  if (!positive(scale) || !positive(k_scale) || !positive(v_scale)) return MISA_ERR_INVALID_ARG;
+  if (!positive(scale) || !factor(k_scale) || !factor(v_scale)) return MISA_ERR_INVALID_ARG;
   if (acc_opt && ld_acc < L) return MISA_ERR_INVALID_ARG;
   if (T == 0) return MISA_OK;
   if (!q || !at16(q) || !pool || !at16(pool) || !page_table || !n || !out || !at16(out)) return MISA_ERR_INVALID_ARG;
@@ -152,12 +155,12 @@ misa_status misa_kv4_compact(void* pool, int64_t num_pages, int page_size, const
   if (keep > kMaxLen) return MISA_ERR_UNSUPPORTED;
   if (T == 0) return MISA_OK;
   if (!pool || !at16(pool) || !page_table || !idx) return MISA_ERR_INVALID_ARG;
-  const int64_t row = (int64_t)H_kv * 2 * (9 * d / 16);
-  if (!ws || ws_bytes < misa::compact_ws_bytes(T, keep, row) || (reinterpret_cast<uintptr_t>(ws) & 255))
+  if (!ws || ws_bytes < misa::compact_ws_bytes(T, keep, 2 * H_kv, d / 2, d / 16) || (reinterpret_cast<uintptr_t>(ws) & 255))
     return MISA_ERR_WORKSPACE;
   const Kv4Pool p = to_pool(pool, num_pages, page_size, page_table, max_pages, H_kv, d);
-  misa::launch_compact_rows(p, 2 * H_kv, p.slab_bytes(), d / 2, d / 16, idx, T, keep, ws,
-                            static_cast<cudaStream_t>(stream));
+  if (!misa::launch_compact_rows(p, 2 * H_kv, p.slab_bytes(), d / 2, d / 16, idx, T, keep, ws,
+                                 static_cast<cudaStream_t>(stream)))
+    return MISA_ERR_CUDA;
   return launch_status();
 }
 
@@ -173,7 +176,7 @@ misa_status misa_keys_compact_paged(void* pool, int64_t num_pages, int page_size
   if (T == 0) return MISA_OK;
   if (!pool || !at16(pool) || !page_table || !idx) return MISA_ERR_INVALID_ARG;
   const int rb = d * (dtype == MISA_F32 ? 4 : 2);
-  if (!ws || ws_bytes < misa::compact_ws_bytes(T, keep, rb) || (reinterpret_cast<uintptr_t>(ws) & 255))
+  if (!ws || ws_bytes < misa::compact_ws_bytes(T, keep, 1, rb, 0) || (reinterpret_cast<uintptr_t>(ws) & 255))
     return MISA_ERR_WORKSPACE;
   misa::RowPages p;
   p.base = static_cast<uint8_t*>(pool);
@@ -181,7 +184,8 @@ misa_status misa_keys_compact_paged(void* pool, int64_t num_pages, int page_size
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   p.page_size = page_size;
-  misa::launch_compact_rows(p, 1, (int64_t)page_size * rb, rb, 0, idx, T, keep, ws, static_cast<cudaStream_t>(stream));
+  if (!misa::launch_compact_rows(p, 1, (int64_t)page_size * rb, rb, 0, idx, T, keep, ws, static_cast<cudaStream_t>(stream)))
+    return MISA_ERR_CUDA;
   return launch_status();
 }
 

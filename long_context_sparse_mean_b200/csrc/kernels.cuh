@@ -208,8 +208,9 @@ void launch_kv4_read(DType dt, const Kv4Pool& pool, const int32_t* cu, const int
 // Closes up the rows of every sequence in place: row idx[t, j] moves to row j (idx ascending, -1 behind
 // the last).  Rows of a page are rb bytes in each of `slabs` slabs of slab_bytes, and behind those
 // page_size scale rows of sb bytes (0, 4 or 8).
-size_t compact_ws_bytes(int T, int keep, int64_t row_bytes);
-void launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, int rb, int sb, const int32_t* idx,
+// ws: one mark per sequence, group of slabs and segment of rows (cleared by the call).
+size_t compact_ws_bytes(int T, int keep, int slabs, int rb, int sb);
+bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, int rb, int sb, const int32_t* idx,
                          int T, int keep, void* ws, cudaStream_t s);
 
 // Attention of query t over its sequence's tokens in a 4-bit cache, or over the tokens idx[t][0 .. P)
@@ -231,6 +232,7 @@ bool launch_prompt_attention(const void* q, const void* k, const void* v, int64_
                              float scale, void* out, float* lse, cudaStream_t s);
 
 int read_and_clear_prompt_status();  // as read_and_clear_tc_status
+int read_and_clear_compact_status();
 bool read_and_clear_bad_ids_kv4_cache(unsigned int* out);
 bool read_and_clear_bad_ids_kv4_attn(unsigned int* out);
 

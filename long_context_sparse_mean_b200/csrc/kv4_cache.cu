@@ -1,13 +1,13 @@
 // The 4-bit caches' upkeep (format in kv4.cuh): rows written as they are computed, read back, and
 // closed up after an eviction.
+#include <algorithm>
+
 #include "kernels.cuh"
 #include "kv4.cuh"
 
 namespace misa {
 
 namespace {
-
-constexpr int64_t kCompactWsBytes = 32ll << 20;  // workspace of a compaction: stays in the L2 (126 MB)
 
 // Sequence of packed row r: the last b with cu[b] <= r, or -1 when the row lies outside
 // [cu[0], cu[S]).  Sequences without rows are passed over.
@@ -22,183 +22,334 @@ __device__ __forceinline__ int packed_seq(const int32_t* __restrict__ cu, int S,
   return lo;
 }
 
-template <DType DT>
-__device__ __forceinline__ void load_block16(const void* base, int64_t at, float (&x)[16]) {
-  if (DT == DType::BF16) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 u = __ldg(p + i);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[8 * i + 2 * e] = bf16_lo(w[e]);
-        x[8 * i + 2 * e + 1] = bf16_hi(w[e]);
-      }
-    }
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 u = __ldg(p + i);
-      x[4 * i] = u.x;
-      x[4 * i + 1] = u.y;
-      x[4 * i + 2] = u.z;
-      x[4 * i + 3] = u.w;
-    }
-  }
+// x / b to nearest for finite b away from the ends of fp32's range, given y = 1 / b to nearest (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990: the residual of the
+// first quotient is exact in one fused multiply-add, and a second adds it in).  Quotients past 8 keep
+// their sign and stay past 8, infinite x included, which is all that the conversion to e2m1 needs.
+__device__ __forceinline__ float divide(float x, float b, float y) {
+  const float q = fminf(fmaxf(x * y, -8.f), 8.f);
+  return fmaf(fmaf(-q, b, x), y, q);
 }
 
-// One thread per 16-element block of (row, head, side).
-template <DType DT>
+// Both kernels: four threads a row of a head and side; thread c has the elements 16 j + 4 c .. + 3 of every
+// block j, which are chunk c of the code row, so codes move in whole 16-byte (d = 64: 8-byte) words and
+// the elements in 8- or 16-byte pieces of which four threads cover a full 32- or 64-byte stretch.  What
+// bounds them is HBM: every element is read or written once in its own type, every code once.
+template <int D, DType DT>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const void* __restrict__ k, const void* __restrict__ v,
                                                          int64_t ldk, int64_t ldv, Kv4Pool pool,
                                                          const int32_t* __restrict__ cu,
                                                          const int32_t* __restrict__ start, int S, int rows, float kg,
                                                          float vg) {
-  const int nb = pool.d / 16;
+  constexpr int NB = D / 16;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t per = (int64_t)pool.Hkv * 2 * nb;
-  const int64_t r = i / per;
-  if (r >= rows) return;
-  const int u = (int)(i - r * per);
-  const int b = u % nb, side = (u / nb) & 1, h = u / (2 * nb);
-  const int seq = packed_seq(cu, S, (int)r);
-  if (seq < 0) return;
-  const int64_t s = (int64_t)__ldg(start + seq) + (r - __ldg(cu + seq));
-  const int64_t pg = kv4_page(pool, seq, s, u == 0);
+  const int c = (int)(i & 3), sides = 2 * pool.Hkv;
+  const int64_t u = i >> 2, r = u / sides;
+  const bool in = r < rows;  // whole groups of four threads alike; they exchange maxima below
+  const int sl = (int)(u - r * sides), h = sl >> 1, side = sl & 1;
+  float x[NB][4];
+  if (in) {
+    const int64_t at = r * (side ? ldv : ldk) + (int64_t)h * D + 4 * c;
+    const void* base = side ? v : k;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      if (DT == DType::BF16) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + at + 16 * j));
+        x[j][0] = bf16_lo(w.x);
+        x[j][1] = bf16_hi(w.x);
+        x[j][2] = bf16_lo(w.y);
+        x[j][3] = bf16_hi(w.y);
+      } else {
+        const float4 w = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + 16 * j));
+        x[j][0] = w.x;
+        x[j][1] = w.y;
+        x[j][2] = w.z;
+        x[j][3] = w.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
+  }
+  const int seq = in ? packed_seq(cu, S, (int)r) : -1;
+  int64_t s = 0, pg = -1;
+  if (seq >= 0) {
+    s = (int64_t)__ldg(start + seq) + (r - __ldg(cu + seq));
+    pg = kv4_page(pool, seq, s, sl == 0 && c == 0);
+  }
+  const float g = side ? vg : kg, g6 = g * 6.0f;
+  uint32_t code[NB / 2], scale[NB / 4];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[j][e] = x[j][e] == x[j][e] ? x[j][e] : 0.f;  // NaN stores as 0
+      top = fmaxf(top, fabsf(x[j][e]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t s8 = float_to_e4m3(top / g6);
+    const float unit = e4m3_to_float(s8) * g, y = unit == 0.f ? 0.f : __frcp_rn(unit);
+    // with unit 0, y is 0 too, and every quotient is x 0 0 = 0
+    const float z = unit == 0.f ? 0.f : 1.f;
+    const uint32_t w = float2_to_e2m1x2(divide(x[j][0] * z, unit, y), divide(x[j][1] * z, unit, y)) |
+                       (float2_to_e2m1x2(divide(x[j][2] * z, unit, y), divide(x[j][3] * z, unit, y)) << 8);
+    code[j / 2] = j & 1 ? code[j / 2] | (w << 16) : w;
+    scale[j / 4] = j & 3 ? scale[j / 4] | (s8 << (8 * (j & 3))) : s8;
+  }
   if (pg < 0) return;
-  float x[16];
-  load_block16<DT>(side ? v : k, r * (side ? ldv : ldk) + (int64_t)h * pool.d + b * 16, x);
-  const float g = side ? vg : kg;
-  float top = 0.f;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    x[e] = x[e] == x[e] ? x[e] : 0.f;  // NaN stores as 0
-    top = fmaxf(top, fabsf(x[e]));
+  uint8_t* slab = pool.base + pg * pool.page_bytes() + (int64_t)sl * pool.slab_bytes();
+  const int at = (int)((uint32_t)s % (uint32_t)pool.page_size);
+  uint8_t* row = slab + (int64_t)at * (D / 2) + c * (D / 8);
+  uint8_t* sc = slab + pool.scales_at() + (int64_t)at * NB;
+  if constexpr (D == 128) {
+    *reinterpret_cast<uint4*>(row) = make_uint4(code[0], code[1], code[2], code[3]);
+    if (c == 0) *reinterpret_cast<uint2*>(sc) = make_uint2(scale[0], scale[1]);
+  } else {
+    *reinterpret_cast<uint2*>(row) = make_uint2(code[0], code[1]);
+    if (c == 0) *reinterpret_cast<uint32_t*>(sc) = scale[0];
   }
-  const uint32_t s8 = float_to_e4m3(top / (g * 6.0f));
-  const float unit = e4m3_to_float(s8) * g;
-  uint8_t* slab = pool.base + pg * pool.page_bytes() + (int64_t)(2 * h + side) * pool.slab_bytes();
-  const int at = (int)(s % pool.page_size);
-  uint8_t* row = slab + (int64_t)at * (pool.d / 2);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    uint32_t code = 0;
-    if (unit != 0.f)
-      code = float2_to_e2m1x2(x[4 * c] / unit, x[4 * c + 1] / unit) |
-             (float2_to_e2m1x2(x[4 * c + 2] / unit, x[4 * c + 3] / unit) << 8);
-    *reinterpret_cast<uint16_t*>(row + (pool.d / 8) * c + 2 * b) = (uint16_t)code;
-  }
-  slab[pool.scales_at() + (int64_t)at * nb + b] = (uint8_t)s8;
 }
 
-// One thread per 16-element block of (row, head, side).
-template <DType DT>
+template <int D, DType DT>
 __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Pool pool, const int32_t* __restrict__ cu,
                                                        const int32_t* __restrict__ start, int S, int rows, float kg,
                                                        float vg, void* __restrict__ k, void* __restrict__ v) {
-  const int nb = pool.d / 16;
+  constexpr int NB = D / 16;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t per = (int64_t)pool.Hkv * 2 * nb;
-  const int64_t r = i / per;
+  const int c = (int)(i & 3), sides = 2 * pool.Hkv;
+  const int64_t u = i >> 2, r = u / sides;
   if (r >= rows) return;
-  const int u = (int)(i - r * per);
-  const int b = u % nb, side = (u / nb) & 1, h = u / (2 * nb);
+  const int sl = (int)(u - r * sides), h = sl >> 1, side = sl & 1;
   const int seq = packed_seq(cu, S, (int)r);
   if (seq < 0) return;
   const int64_t s = (int64_t)__ldg(start + seq) + (r - __ldg(cu + seq));
-  const int64_t pg = kv4_page(pool, seq, s, u == 0);
-  float x[16];
+  const int64_t pg = kv4_page(pool, seq, s, sl == 0 && c == 0);
+  uint32_t code[NB / 2], scale[NB / 4];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = 0.f;
+  for (int j = 0; j < NB / 2; ++j) code[j] = 0u;
+#pragma unroll
+  for (int j = 0; j < NB / 4; ++j) scale[j] = 0u;
   if (pg >= 0) {
-    const uint8_t* slab = pool.base + pg * pool.page_bytes() + (int64_t)(2 * h + side) * pool.slab_bytes();
-    const int at = (int)(s % pool.page_size);
-    const uint8_t* row = slab + (int64_t)at * (pool.d / 2);
-    const float sc = e4m3_to_float(slab[pool.scales_at() + (int64_t)at * nb + b]), g = side ? vg : kg;
-    uint32_t w[2];
+    const uint8_t* slab = pool.base + pg * pool.page_bytes() + (int64_t)sl * pool.slab_bytes();
+    const int at = (int)((uint32_t)s % (uint32_t)pool.page_size);
+    const uint8_t* row = slab + (int64_t)at * (D / 2) + c * (D / 8);
+    const uint8_t* sc = slab + pool.scales_at() + (int64_t)at * NB;
+    if constexpr (D == 128) {
+      const uint4 w = *reinterpret_cast<const uint4*>(row);
+      const uint2 e = *reinterpret_cast<const uint2*>(sc);
+      code[0] = w.x, code[1] = w.y, code[2] = w.z, code[3] = w.w;
+      scale[0] = e.x, scale[1] = e.y;
+    } else {
+      const uint2 w = *reinterpret_cast<const uint2*>(row);
+      code[0] = w.x, code[1] = w.y;
+      scale[0] = *reinterpret_cast<const uint32_t*>(sc);
+    }
+  }
+  const float g = side ? vg : kg;
+  const int64_t at = (r * pool.Hkv + h) * D + 4 * c;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      w[c] = (uint32_t)*reinterpret_cast<const uint16_t*>(row + (pool.d / 8) * (2 * c) + 2 * b) |
-             ((uint32_t)*reinterpret_cast<const uint16_t*>(row + (pool.d / 8) * (2 * c + 1) + 2 * b) << 16);
+  for (int w = 0; w < NB / 2; ++w) {
+    uint32_t y[4];
+    e2m1x8_to_half2(code[w], y[0], y[1], y[2], y[3]);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      uint32_t y[4];
-      e2m1x8_to_half2(w[c], y[0], y[1], y[2], y[3]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
-        x[8 * c + 2 * e] = f.x * sc * g;
-        x[8 * c + 2 * e + 1] = f.y * sc * g;
+    for (int b = 0; b < 2; ++b) {
+      const int j = 2 * w + b;
+      const float sc = e4m3_to_float((scale[j / 4] >> (8 * (j & 3))) & 255u);
+      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&y[2 * b]));
+      const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&y[2 * b + 1]));
+      const float x0 = p.x * sc * g, x1 = p.y * sc * g, x2 = q.x * sc * g, x3 = q.y * sc * g;
+      if (DT == DType::BF16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(x0, x1), hi = __floats2bfloat162_rn(x2, x3);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(side ? v : k) + at + 16 * j) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(side ? v : k) + at + 16 * j) = make_float4(x0, x1, x2, x3);
       }
     }
   }
-  const int64_t at = ((int64_t)r * pool.Hkv + h) * pool.d + b * 16;
-  if (DT == DType::BF16) {
-    uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(side ? v : k) + at);
-    uint32_t y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-      y[e] = *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Closes up caches in place: row idx[t, j] of sequence t moves to row j, for all j.  A CTA takes a segment
+// of R rows j of one sequence and a group of slabs: it reads their sources into shared memory, marks its
+// segment as read, waits until every segment whose sources lie where it is going to write has been
+// marked, and writes.  idx is ascending, so idx[t, j] >= j: a segment's own place is read by itself and by
+// segments before it alone, which have smaller block indices, started no later, and wait for none after
+// them; they are found by searching idx for the ends of the place while the copies are under way.  (In
+// the usual case of a part kept, rows come from far behind their new place, and the segments waited for
+// finished long ago.)  A short list is one segment and needs no marks.
+// Rows that stay where they are are passed over, and so are rows whose own or source page is not in the
+// pool.  Bound by HBM: rows are read and written once.
+// Waits are bounded (1 s); a segment whose wait runs out is not written and a status word is set.
+constexpr int kSeg = 64;                // rows of a segment where there are several
+constexpr int kGroupBytes = 72 * 1024;  // its rows in shared memory: three CTAs an SM
+constexpr int kOneSeg = 512;            // longest list taken as one segment,
+constexpr int kOneSegBytes = 160 * 1024;  // where a slab's rows of it fit here
+constexpr int kFewCtas = 96;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+
+__device__ int g_compact_status = 0;
+
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+// First position of the ascending list[0 .. count) (entries < 0 lie behind the last) with an entry >= v;
+// the whole warp searches, 32 probes a step.
+__device__ __forceinline__ int first_at_least(const int32_t* list, int count, int v) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = count;  // the answer lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step + step - 1;
+    bool ge = true;
+    if (i < hi) {
+      const int x = __ldg(list + i);
+      ge = x >= v || x < 0;
     }
-    o[0] = make_uint4(y[0], y[1], y[2], y[3]);
-    o[1] = make_uint4(y[4], y[5], y[6], y[7]);
-  } else {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(side ? v : k) + at);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+    const unsigned m = __ballot_sync(0xffffffffu, ge);
+    if (m == 0) return hi;
+    const int f = __ffs(m) - 1;
+    hi = min(hi, lo + f * step + step - 1);
+    lo = lo + f * step;
+  }
+  return lo;
+}
+
+template <int P>  // 16-byte pieces of a row
+__global__ void __launch_bounds__(256) compact_rows_kernel(RowPages pages, int slabs, int group, int64_t slab_bytes,
+                                                           int sb, const int32_t* __restrict__ idx, int keep, int R,
+                                                           uint32_t* __restrict__ read_marks) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int first_wait, end_wait, late;
+  const int seg = blockIdx.x, t = blockIdx.z, s0 = blockIdx.y * group, ns = min(group, slabs - s0);
+  const int j0 = seg * R, warp = threadIdx.x >> 5;
+  constexpr int rb = 16 * P;
+  const int32_t* list = idx + (int64_t)t * keep;
+  const int64_t page_bytes = (int64_t)slabs * slab_bytes, scales_at = (int64_t)pages.page_size * rb;
+  uint32_t* marks = read_marks + ((int64_t)t * gridDim.y + blockIdx.y) * gridDim.x;
+  uint8_t* const rows = smem;                                // [slab][row][rb]
+  uint8_t* const sc = rows + (int64_t)ns * R * rb;           // [slab][row][sb]
+  int4* const place = reinterpret_cast<int4*>(smem + (int64_t)group * R * (rb + sb));  // source page, slot; own page, slot
+  bool any = false;
+  for (int r = threadIdx.x; r < R; r += 256) {
+    const int j = j0 + r, src = j < keep ? __ldg(list + j) : -1;
+    int64_t pf = -1, pt = -1;
+    if (src >= 0 && src != j) {
+      pf = kv4_page(pages, t, src, blockIdx.y == 0);
+      pt = kv4_page(pages, t, j, false);
+    }
+    const bool ok = pf >= 0 && pt >= 0;
+    any |= ok;
+    place[r] = make_int4(ok ? (int)pf : -1, (int)((uint32_t)src % (uint32_t)pages.page_size), (int)pt,
+                         (int)((uint32_t)j % (uint32_t)pages.page_size));
+  }
+  if (threadIdx.x == 0) late = 0;
+  const bool moves = __syncthreads_or(any);
+  uint8_t* const base = pages.base + s0 * slab_bytes;
+  if (moves) {
+    for (int u = threadIdx.x; u < R * P; u += 256) {
+      const int r = u / P, piece = u % P;
+      const int4 w = place[r];
+      if (w.x < 0) continue;
+      const uint8_t* p = base + w.x * page_bytes + (int64_t)w.y * rb + piece * 16;
+      for (int x = 0; x < ns; ++x) copy16_async(rows + ((int64_t)x * R + r) * rb + piece * 16, p + x * slab_bytes);
+    }
+    if (sb) {
+      for (int u = threadIdx.x; u < R * 8; u += 256) {  // eight threads a row, each every eighth slab
+        const int r = u >> 3;
+        const int4 w = place[r];
+        if (w.x < 0) continue;
+        for (int x = u & 7; x < ns; x += 8) {
+          const uint8_t* p = base + w.x * page_bytes + x * slab_bytes + scales_at + (int64_t)w.y * sb;
+          const uint32_t q = (uint32_t)__cvta_generic_to_shared(sc + ((int64_t)x * R + r) * sb);
+          if (sb == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(q), "l"(p) : "memory");
+          else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(q), "l"(p) : "memory");
+        }
+      }
+    }
+    if (gridDim.x > 1 && warp < 2) {  // segments with sources in [j0, j0 + R), this one aside
+      const int at = first_at_least(list, keep, warp ? j0 + R : j0);
+      if ((threadIdx.x & 31) == 0) (warp ? end_wait : first_wait) = warp ? min(seg, (at + R - 1) / R) : at / R;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  __syncthreads();  // the segment has been read
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      __threadfence();
+      atomicExch(marks + seg, 1u);
+    }
+    if (!moves) return;
+    if (warp == 0) {
+      for (int x = first_wait + (int)threadIdx.x; x < end_wait; x += 32) {
+        const volatile uint32_t* m = marks + x;
+        if (*m) continue;
+        uint64_t t0, t1;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+        while (!*m) {
+          __nanosleep(64);
+          asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
+          if (t1 - t0 > kWaitLimitNs) {
+            late = 1;
+            break;
+          }
+        }
+      }
+      __threadfence();
+    }
+    __syncthreads();
+    if (late) {
+      if (threadIdx.x == 0) atomicExch(&g_compact_status, 1);
+      return;
+    }
+  }
+  for (int u = threadIdx.x; u < R * P; u += 256) {
+    const int r = u / P, piece = u % P;
+    const int4 w = place[r];
+    if (w.x < 0) continue;
+    uint8_t* p = base + w.z * page_bytes + (int64_t)w.w * rb + piece * 16;
+#pragma unroll 4
+    for (int x = 0; x < ns; ++x)
+      *reinterpret_cast<uint4*>(p + x * slab_bytes) = *reinterpret_cast<const uint4*>(rows + ((int64_t)x * R + r) * rb + piece * 16);
+  }
+  if (sb) {
+    for (int u = threadIdx.x; u < R * 8; u += 256) {
+      const int r = u >> 3;
+      const int4 w = place[r];
+      if (w.x < 0) continue;
+      for (int x = u & 7; x < ns; x += 8) {
+        uint8_t* p = base + w.z * page_bytes + x * slab_bytes + scales_at + (int64_t)w.w * sb;
+        const uint8_t* q = sc + ((int64_t)x * R + r) * sb;
+        if (sb == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(q);
+        else *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(q);
+      }
+    }
   }
 }
 
-// Rows [j0, j0 + C) of every sequence's kept list, between the pool and the workspace
-// [T][C][slabs][row bytes].  Moving a chunk takes two launches: the first copies rows idx[t, j] out, the
-// second writes them to rows j.  idx is ascending, so idx[t, j] >= j: a chunk's writes land on rows
-// below every row that a later chunk reads, and every earlier chunk has been read already.  Rows that
-// stay where they are (idx[t, j] == j) are not touched.
-// A unit is 16 bytes of a code row, or the whole scale row (sb bytes, 4 or 8; 0: the pool has none).
-template <bool OUT>
-__global__ void __launch_bounds__(256) compact_rows_kernel(RowPages pages, int slabs, int64_t slab_bytes,
-                                                           int rb, int sb, const int32_t* __restrict__ idx, int T,
-                                                           int keep, int j0, int C, uint8_t* __restrict__ ws) {
-  const int units = rb / 16 + (sb ? 1 : 0);
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t per = (int64_t)slabs * C * units;
-  const int64_t t = i / per;
-  if (t >= T) return;
-  int64_t x = i - t * per;
-  const int slab = (int)(x / ((int64_t)C * units));
-  x -= (int64_t)slab * C * units;
-  const int jj = (int)(x / units), u = (int)(x - (int64_t)jj * units);
-  const int j = j0 + jj;
-  if (j >= keep) return;
-  const int src = __ldg(idx + t * keep + j);
-  if (src < 0 || src == j) return;
-  // a row whose source or own place the table does not hold stays as it is
-  const bool count = OUT && slab == 0 && u == 0;
-  const int64_t pj = kv4_page(pages, t, j, false), ps = kv4_page(pages, t, src, count);
-  if (pj < 0 || ps < 0) return;
-  const int64_t s = OUT ? src : j, pg = OUT ? ps : pj;
-  const int at = (int)(s % pages.page_size);
-  uint8_t* base = pages.base + (pg * slabs + slab) * slab_bytes;
-  uint8_t* w = ws + (t * slabs + slab) * C * (int64_t)(rb + sb);
-  if (u * 16 < rb) {
-    uint4* a = reinterpret_cast<uint4*>(base + (int64_t)at * rb + u * 16);
-    uint4* b = reinterpret_cast<uint4*>(w + (int64_t)jj * rb + u * 16);
-    if (OUT) *b = *a;
-    else *a = *b;
-  } else {
-    uint8_t* a = base + (int64_t)pages.page_size * rb + (int64_t)at * sb;
-    uint8_t* b = w + (int64_t)C * rb + (int64_t)jj * sb;
-    if (sb == 8) {
-      if (OUT) *reinterpret_cast<uint2*>(b) = *reinterpret_cast<const uint2*>(a);
-      else *reinterpret_cast<uint2*>(a) = *reinterpret_cast<const uint2*>(b);
-    } else {
-      if (OUT) *reinterpret_cast<uint32_t*>(b) = *reinterpret_cast<const uint32_t*>(a);
-      else *reinterpret_cast<uint32_t*>(a) = *reinterpret_cast<const uint32_t*>(b);
-    }
+// How a compaction is cut up: rows of a segment, slabs of a group, segments, groups, shared memory.
+struct CompactPlan {
+  int R, group, segs, groups;
+  size_t smem;
+};
+
+CompactPlan compact_plan(int T, int slabs, int rb, int sb, int keep) {
+  CompactPlan p;
+  const int row = rb + sb;
+  int64_t room = kGroupBytes;
+  p.R = kSeg;
+  if (keep <= kOneSeg && (int64_t)keep * row <= kOneSegBytes) {
+    p.R = (keep + 15) / 16 * 16;
+    room = std::max<int64_t>(room, (int64_t)p.R * row);
   }
+  p.group = (int)std::min<int64_t>(slabs, std::max<int64_t>(1, room / ((int64_t)p.R * row)));
+  // a call of few CTAs takes a slab each: their number is what its time depends on
+  if ((int64_t)T * ((keep + p.R - 1) / p.R) * ((slabs + p.group - 1) / p.group) < kFewCtas) p.group = 1;
+  p.segs = (keep + p.R - 1) / p.R;
+  p.groups = (slabs + p.group - 1) / p.group;
+  p.smem = (size_t)p.R * p.group * row + sizeof(int4) * p.R;
+  return p;
 }
 
 }  // namespace
@@ -206,48 +357,66 @@ __global__ void __launch_bounds__(256) compact_rows_kernel(RowPages pages, int s
 void launch_kv4_append(DType dt, const void* k, const void* v, int64_t ldk, int64_t ldv, const Kv4Pool& pool,
                        const int32_t* cu, const int32_t* start, int S, int rows, float kg, float vg, cudaStream_t s) {
   if (S <= 0 || rows <= 0) return;
-  const int64_t threads = (int64_t)rows * pool.Hkv * 2 * (pool.d / 16);
-  const unsigned grid = (unsigned)((threads + 255) / 256);
-  if (dt == DType::BF16)
-    kv4_append_kernel<DType::BF16><<<grid, 256, 0, s>>>(k, v, ldk, ldv, pool, cu, start, S, rows, kg, vg);
-  else
-    kv4_append_kernel<DType::F32><<<grid, 256, 0, s>>>(k, v, ldk, ldv, pool, cu, start, S, rows, kg, vg);
+  const unsigned grid = (unsigned)(((int64_t)rows * pool.Hkv * 2 * 4 + 255) / 256);
+  auto run = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(k, v, ldk, ldv, pool, cu, start, S, rows, kg, vg); };
+  if (pool.d == 128) dt == DType::BF16 ? run(kv4_append_kernel<128, DType::BF16>) : run(kv4_append_kernel<128, DType::F32>);
+  else dt == DType::BF16 ? run(kv4_append_kernel<64, DType::BF16>) : run(kv4_append_kernel<64, DType::F32>);
 }
 
 void launch_kv4_read(DType dt, const Kv4Pool& pool, const int32_t* cu, const int32_t* start, int S, int rows,
                      float kg, float vg, void* k, void* v, cudaStream_t s) {
   if (S <= 0 || rows <= 0) return;
-  const int64_t threads = (int64_t)rows * pool.Hkv * 2 * (pool.d / 16);
-  const unsigned grid = (unsigned)((threads + 255) / 256);
-  if (dt == DType::BF16)
-    kv4_read_kernel<DType::BF16><<<grid, 256, 0, s>>>(pool, cu, start, S, rows, kg, vg, k, v);
-  else
-    kv4_read_kernel<DType::F32><<<grid, 256, 0, s>>>(pool, cu, start, S, rows, kg, vg, k, v);
+  const unsigned grid = (unsigned)(((int64_t)rows * pool.Hkv * 2 * 4 + 255) / 256);
+  auto run = [&](auto kernel) { kernel<<<grid, 256, 0, s>>>(pool, cu, start, S, rows, kg, vg, k, v); };
+  if (pool.d == 128) dt == DType::BF16 ? run(kv4_read_kernel<128, DType::BF16>) : run(kv4_read_kernel<128, DType::F32>);
+  else dt == DType::BF16 ? run(kv4_read_kernel<64, DType::BF16>) : run(kv4_read_kernel<64, DType::F32>);
 }
 
-// Rows per chunk of a compaction: what fits the workspace piece (at least one row of every sequence).
-int compact_chunk(int T, int keep, int64_t row_bytes) {
-  const int64_t fit = kCompactWsBytes / (row_bytes * T) / 16 * 16;
-  return (int)(fit < 16 ? 16 : (fit < keep ? fit : (keep + 15) / 16 * 16));
+size_t compact_ws_bytes(int T, int keep, int slabs, int rb, int sb) {
+  const CompactPlan p = compact_plan(T, slabs, rb, sb, keep);
+  return sizeof(uint32_t) * (size_t)T * p.groups * p.segs;
 }
 
-size_t compact_ws_bytes(int T, int keep, int64_t row_bytes) {
-  return (size_t)T * compact_chunk(T, keep, row_bytes) * row_bytes;
-}
-
-void launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, int rb, int sb, const int32_t* idx,
+bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, int rb, int sb, const int32_t* idx,
                          int T, int keep, void* ws, cudaStream_t s) {
-  if (T <= 0 || keep <= 0) return;
-  const int C = compact_chunk(T, keep, (int64_t)slabs * (rb + sb));
-  const int units = rb / 16 + (sb ? 1 : 0);
-  for (int j0 = 0; j0 < keep; j0 += C) {
-    const int64_t threads = (int64_t)T * slabs * C * units;
-    const unsigned grid = (unsigned)((threads + 255) / 256);
-    compact_rows_kernel<true><<<grid, 256, 0, s>>>(pages, slabs, slab_bytes, rb, sb, idx, T, keep, j0, C,
-                                                   static_cast<uint8_t*>(ws));
-    compact_rows_kernel<false><<<grid, 256, 0, s>>>(pages, slabs, slab_bytes, rb, sb, idx, T, keep, j0, C,
-                                                    static_cast<uint8_t*>(ws));
+  if (T <= 0 || keep <= 0) return true;
+  const CompactPlan p = compact_plan(T, slabs, rb, sb, keep);
+  if (p.segs > 1 && cudaMemsetAsync(ws, 0, compact_ws_bytes(T, keep, slabs, rb, sb), s) != cudaSuccess) return false;
+  auto run = [&](auto kernel) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOneSegBytes + 16384) != cudaSuccess)
+      return false;
+    constexpr int kMostZ = 65535;
+    for (int t0 = 0; t0 < T; t0 += kMostZ) {
+      RowPages q = pages;
+      q.table += (int64_t)t0 * pages.max_pages;
+      kernel<<<dim3(p.segs, p.groups, std::min(T - t0, kMostZ)), 256, p.smem, s>>>(
+          q, slabs, p.group, slab_bytes, sb, idx + (int64_t)t0 * keep, keep, p.R,
+          static_cast<uint32_t*>(ws) + (int64_t)t0 * p.groups * p.segs);
+    }
+    return true;
+  };
+  switch (rb) {
+    case 32:
+      return run(compact_rows_kernel<2>);
+    case 64:
+      return run(compact_rows_kernel<4>);
+    case 256:
+      return run(compact_rows_kernel<16>);
+    case 512:
+      return run(compact_rows_kernel<32>);
+    default:
+      return false;
   }
+}
+
+int read_and_clear_compact_status() {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_compact_status, sizeof(int)) != cudaSuccess) return -1;
+  if (v) {
+    const int zero = 0;
+    cudaMemcpyToSymbol(g_compact_status, &zero, sizeof(int));
+  }
+  return v;
 }
 
 MISA_BAD_ID_READER(read_and_clear_bad_ids_kv4_cache)

@@ -54,6 +54,7 @@ def test_cache_refusals(lib, name, base):
                      (dict(dt=3), UNSUPPORTED), (dict(np=1 << 40), UNSUPPORTED), (dict(H=0), INVALID),
                      (dict(S=-1), INVALID), (dict(rows=-1), INVALID), (dict(np=0), INVALID), (dict(mp=0), INVALID),
                      (dict(kg=0.0), INVALID), (dict(vg=-1.0), INVALID), (dict(kg=NAN), INVALID), (dict(vg=INF), INVALID),
+                     (dict(kg=2.0 ** -61), INVALID), (dict(vg=2.0 ** 61), INVALID),
                      (dict(pool=None), INVALID), (dict(pool=BENT), INVALID), (dict(table=None), INVALID),
                      (dict(cu=None), INVALID), (dict(start=None), INVALID), (dict(k=None), INVALID),
                      (dict(v=BENT), INVALID), (dict(rows=1 << 30), UNSUPPORTED),
@@ -87,11 +88,11 @@ def test_eviction_refusals(lib):
         assert call(lib.misa_evict_select, EVICT, **kw) == want, kw
     for kw, want in [(dict(keep=0), INVALID), (dict(keep=641), INVALID), (dict(d=100), UNSUPPORTED), (dict(ps=8), UNSUPPORTED),
                      (dict(idx=None), INVALID), (dict(pool=BENT), INVALID), (dict(ws=None), WORKSPACE),
-                     (dict(wsb=64), WORKSPACE), (dict(T=0, idx=None), OK)]:
+                     (dict(ws=BENT), WORKSPACE), (dict(wsb=4), WORKSPACE), (dict(T=0, idx=None), OK)]:
         assert call(lib.misa_kv4_compact, COMPACT, **kw) == want, kw
     for kw, want in [(dict(keep=0), INVALID), (dict(keep=641), INVALID), (dict(d=64), UNSUPPORTED), (dict(dt=5), UNSUPPORTED),
-                     (dict(idx=None), INVALID), (dict(pool=BENT), INVALID), (dict(ws=BENT), WORKSPACE),
-                     (dict(wsb=64), WORKSPACE), (dict(T=0, idx=None), OK)]:
+                     (dict(idx=None), INVALID), (dict(pool=BENT), INVALID), (dict(ws=None), WORKSPACE),
+                     (dict(ws=BENT), WORKSPACE), (dict(wsb=4), WORKSPACE), (dict(T=0, idx=None), OK)]:
         assert call(lib.misa_keys_compact_paged, KEYS, **kw) == want, kw
 
 
@@ -112,9 +113,6 @@ def test_workspace_sizes(lib):
     assert weights >= plain + 4 * 32 * 1000 * 4  # the logits
     assert ws(11, 4, 1 << 20, 32, 8, 128, 0, 0) == plain  # without weights it does not grow with the length
     assert ws(11, 4, 1 << 20, 32, 8, 128, 64, 1) < weights
-    assert ws(12, 4, 0, 8, 0, 128, 100, 0) >= 4 * 100 * 8 * 2 * 72
-    assert ws(12, 4, 0, 8, 0, 128, 10 ** 6, 0) <= 64 << 20  # bounded: the rows move in chunks
-    assert ws(13, 4, 0, 0, 0, 256, 100, 0) >= 4 * 100 * 256
 
 
 def _t(*s, dtype=torch.bfloat16):

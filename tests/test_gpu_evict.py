@@ -69,7 +69,7 @@ def test_lengths_outside_the_row_and_limits():
 @pytest.mark.parametrize("Hkv,d,page,lens,keep", [
     (2, 128, 16, [100, 37, 0, 64], 40),
     (3, 64, 48, [500, 499], 200),
-    (8, 128, 64, [30000, 25000], 20000),   # more than one chunk of the workspace
+    (8, 128, 64, [30000, 25000], 20000),   # many segments of rows, more than the GPU runs at once
 ])
 def test_caches_close_up_in_place(Hkv, d, page, lens, keep):
     M = lib()
@@ -126,9 +126,10 @@ def test_eviction_captured():
     acc, n = cuda(rng.random((2, 3000)).astype(np.float32)), cuda(np.array([3000, 1500], np.int32))
     table = cuda(np.arange(2 * 188, dtype=np.int32).reshape(2, 188))
     pool = cuda(rng.integers(0, 256, (376, 2, 2, 16 * 36), dtype=np.uint8))
-    ws = M.Workspace()
     idx, no, ao = (torch.empty(2, 700, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda"),
                    torch.empty(2, 700, device="cuda"))
+
+    ws = M.Workspace()
 
     def step(p):
         M.misa_evict_select(acc, n, 700, 4, 50, idx=idx, n_out=no, acc_out=ao)
