@@ -19,6 +19,7 @@ Tensor conventions (all on one CUDA device, contiguous):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -284,6 +285,7 @@ def release_default_workspaces() -> None:
     if _default_ws:
         torch.cuda.synchronize()
     _default_ws.clear()
+    _by_handle.clear()
 
 
 def misa_pool_keys(k: torch.Tensor, B: int, kbar: Optional[torch.Tensor] = None, block_begin: int = 0,
@@ -794,6 +796,49 @@ def misa_indexer_paged(q, w, pool, page_table, kbar, n, B: int, h: int, topk: in
 
 
 # ---- attention beside the indexer: 4-bit caches, their attention and eviction, prompt attention ------
+#
+# Decode steps make these calls every few microseconds, so their marshalling is kept short: one check per
+# tensor, raw stream handles, pointers passed as integers.
+
+def _current(t: torch.Tensor, name: str) -> int:
+    """Index of the current CUDA device, where the library launches (t: the call's first tensor)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch._C._cuda_getDevice()
+
+
+def _ready(t: Optional[torch.Tensor], name: str, dtype, cur: int):
+    """Data pointer of a contiguous tensor of this type on the current device (None for None)."""
+    if t is None:
+        return None
+    if t.get_device() != cur or t.dtype is not dtype or not t.is_contiguous():
+        _need(t, name, dtype)
+        _on_device(t)
+    return t.data_ptr()
+
+
+def _handle(stream, cur: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream
+
+
+_by_handle = {}  # (device index, stream handle) -> the default Workspace of that stream
+
+
+def _scratch(ws: Optional["Workspace"], t: torch.Tensor, cur: int, nbytes: int, stream, handle: int):
+    """Pointer of nbytes of the caller's Workspace, or of the stream's default one."""
+    if ws is None:
+        ws = _by_handle.get((cur, handle))
+        if ws is None:
+            ws = _by_handle[(cur, handle)] = _ws(None, t.device, stream)
+    if ws.buf is None or ws.buf.numel() < nbytes or ws._home != handle:
+        ws.get(nbytes, stream)
+    return ws.buf.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(*sizes) -> int:
+    return int(_lib.misa_workspace_bytes(*sizes))
+
 
 def misa_kv4_pool(num_pages: int, page_size: int, H_kv: int, d: int, device="cuda") -> torch.Tensor:
     """An empty pool of 4-bit key and value pages, uint8 [num_pages, H_kv, 2, page_size * 9 d / 16]."""
@@ -808,26 +853,35 @@ def _kv4_geometry(pool, page_table, rows: int, d: int):
     s = pool.shape
     if len(s) != 4 or s[2] != 2 or s[3] <= 0 or (s[3] * 16) % (9 * d) != 0:
         raise ValueError(f"pool must be [num_pages, H_kv, 2, page_size * {9 * d} / 16], got {tuple(s)}")
-    _matrix(page_table, "page_table", rows)
-    return s[0], s[1], s[3] * 16 // (9 * d), page_table.shape[1]
+    ts = page_table.shape
+    if len(ts) != 2 or ts[0] < rows:
+        _matrix(page_table, "page_table", rows)
+    return s[0], s[1], s[3] * 16 // (9 * d), ts[1]
 
 
-def _packed_rows(t, name: str, dtype=None):
+def _packed_rows(t, name: str) -> int:
     """Row stride in elements of packed rows [rows, H, d]: rows may be strided (a slice of a fused
     projection), the elements of a row may not."""
     if t.dim() != 3:
         raise ValueError(f"{name} must be [rows, H, d], got {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     rows, H, d = t.shape
-    if t.numel() == 0 or (rows == 1 and t[0].is_contiguous()):
+    if t.is_contiguous() or t.numel() == 0 or (rows == 1 and t[0].is_contiguous()):
         return H * d
     if t.stride(2) != 1 or (H > 1 and t.stride(1) != d) or t.stride(0) < H * d or t.stride(0) * t.element_size() % 16:
         raise ValueError(f"{name} must have contiguous rows at a stride of a multiple of 16 bytes, got strides "
                          f"{tuple(t.stride())}")
     return t.stride(0)
+
+
+def _rows_ready(t, name: str, dtype, cur: int) -> int:
+    """Data pointer of packed rows that _packed_rows has looked over."""
+    if t.get_device() != cur or t.dtype is not dtype:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        _on_device(t)
+    return t.data_ptr()
 
 
 def _packed(cu, start, name: str = "cu") -> int:
@@ -840,11 +894,16 @@ def _packed(cu, start, name: str = "cu") -> int:
     return S
 
 
+def _lengths(n, T: int) -> None:
+    if n.dim() != 1 or n.shape[0] < T:
+        raise ValueError(f"n must be [>= {T}], got {tuple(n.shape)}")
+
+
 def misa_kv4_append(k, v, pool, page_table, cu, start, k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Write packed rows k, v [rows, H_kv, d] into a 4-bit cache: row r of sequence b (cu[b] <= r <
     cu[b + 1]) at its logical position start[b] + r - cu[b].  k_scale and v_scale: one factor per
     tensor, the same in every call on this cache."""
-    ldk, ldv = _packed_rows(k, "k"), _packed_rows(v, "v", k.dtype)
+    ldk, ldv = _packed_rows(k, "k"), _packed_rows(v, "v")
     if k.shape != v.shape:
         raise ValueError(f"k and v must have one shape, got {tuple(k.shape)} and {tuple(v.shape)}")
     rows, H_kv, d = k.shape
@@ -852,14 +911,13 @@ def misa_kv4_append(k, v, pool, page_table, cu, start, k_scale: float = 1.0, v_s
     num_pages, Hp, page_size, max_pages = _kv4_geometry(pool, page_table, S, d)
     if Hp != H_kv:
         raise ValueError(f"the pool holds {Hp} kv heads, k has {H_kv}")
-    _need(pool, "pool", torch.uint8)
-    _need(page_table, "page_table", torch.int32)
-    _need(cu, "cu", torch.int32)
-    _need(start, "start", torch.int32)
-    _on_device(k, v, pool, page_table, cu, start)
+    cur = _current(k, "k")
+    code = _dtype_code(k)
     _check("misa_kv4_append", _lib.misa_kv4_append(
-        _p(k), _p(v), ldk, ldv, _dtype_code(k), k_scale, v_scale, _p(pool), num_pages, page_size, _p(page_table),
-        max_pages, _p(cu), _p(start), S, rows, H_kv, d, _stream(stream)))
+        _rows_ready(k, "k", k.dtype, cur), _rows_ready(v, "v", k.dtype, cur), ldk, ldv, code, k_scale, v_scale,
+        _ready(pool, "pool", torch.uint8, cur), num_pages, page_size, _ready(page_table, "page_table", torch.int32, cur),
+        max_pages, _ready(cu, "cu", torch.int32, cur), _ready(start, "start", torch.int32, cur), S, rows, H_kv, d,
+        _handle(stream, cur)))
 
 
 def misa_kv4_read(pool, page_table, cu, start, rows: int, d: int, dtype=torch.bfloat16, k_scale: float = 1.0,
@@ -871,20 +929,16 @@ def misa_kv4_read(pool, page_table, cu, start, rows: int, d: int, dtype=torch.bf
     for t, name in ((k, "k"), (v, "v")):
         if t is not None and tuple(t.shape) != (rows, H_kv, d):
             raise ValueError(f"{name} must be {[rows, H_kv, d]}, got {tuple(t.shape)}")
-    _need(pool, "pool", torch.uint8)
-    _need(page_table, "page_table", torch.int32)
-    _need(cu, "cu", torch.int32)
-    _need(start, "start", torch.int32)
-    _need_opt(k, "k", dtype)
-    _need_opt(v, "v", dtype)
-    _on_device(pool, page_table, cu, start, k, v)
+    cur = _current(pool, "pool")
+    pp, tp = _ready(pool, "pool", torch.uint8, cur), _ready(page_table, "page_table", torch.int32, cur)
+    cp, sp = _ready(cu, "cu", torch.int32, cur), _ready(start, "start", torch.int32, cur)
     if k is None:
         k = torch.empty((rows, H_kv, d), dtype=dtype, device=pool.device)
     if v is None:
         v = torch.empty((rows, H_kv, d), dtype=dtype, device=pool.device)
     _check("misa_kv4_read", _lib.misa_kv4_read(
-        _p(pool), num_pages, page_size, _p(page_table), max_pages, _p(cu), _p(start), S, rows, H_kv, d,
-        _dtype_code(k), k_scale, v_scale, _p(k), _p(v), _stream(stream)))
+        pp, num_pages, page_size, tp, max_pages, cp, sp, S, rows, H_kv, d, _dtype_code(k), k_scale, v_scale,
+        _ready(k, "k", dtype, cur), _ready(v, "v", dtype, cur), _handle(stream, cur)))
     return k, v
 
 
@@ -901,8 +955,7 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
     num_pages, H_kv, page_size, max_pages = _kv4_geometry(pool, page_table, T, d)
     if L is None:  # the longest prefix that the table (and acc) can hold
         L = max_pages * page_size if acc is None else min(max_pages * page_size, acc.shape[-1])
-    if n.dim() != 1 or n.shape[0] < T:
-        raise ValueError(f"n must be [>= {T}], got {tuple(n.shape)}")
+    _lengths(n, T)
     if idx is not None:
         _matrix(idx, "idx", T)
     if out is not None and tuple(out.shape) != (T, H_q, d):
@@ -911,26 +964,23 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
         _matrix(lse, "lse", T, H_q)
     if acc is not None:
         _matrix(acc, "acc", T, min_cols=L)
-    _need(q, "q")
-    _need(pool, "pool", torch.uint8)
-    _need(page_table, "page_table", torch.int32)
-    _need(n, "n", torch.int32)
-    _need_opt(idx, "idx", torch.int32)
-    _need_opt(out, "out", q.dtype)
-    _need_opt(lse, "lse", torch.float32)
-    _need_opt(acc, "acc", torch.float32)
-    _on_device(q, pool, page_table, n, idx, out, lse, acc)
+    cur = _current(q, "q")
+    code = _dtype_code(q)
+    qp, pp = _ready(q, "q", q.dtype, cur), _ready(pool, "pool", torch.uint8, cur)
+    tp, np_ = _ready(page_table, "page_table", torch.int32, cur), _ready(n, "n", torch.int32, cur)
+    ip, ap = _ready(idx, "idx", torch.int32, cur), _ready(acc, "acc", torch.float32, cur)
     P = 0 if idx is None else idx.shape[1]
     if out is None:
         out = torch.empty_like(q)
     if lse is None and want_lse:
         lse = torch.empty((T, H_q), dtype=torch.float32, device=q.device)
-    nbytes = misa_workspace_bytes(OP_KV4_ATTENTION, T, L, H_q, H_kv, d, P, int(acc is not None))
-    buf = _ws(ws, q.device, stream).get(nbytes, stream)
+    h = _handle(stream, cur)
+    nbytes = _ws_bytes(OP_KV4_ATTENTION, T, L, H_q, H_kv, d, P, int(acc is not None))
     _check("misa_kv4_attention", _lib.misa_kv4_attention(
-        _p(q), _p(pool), num_pages, page_size, _p(page_table), max_pages, _p(n), _p(idx), T, L, P, H_q, H_kv, d,
-        _dtype_code(q), d ** -0.5 if scale is None else scale, k_scale, v_scale, _p(out), _p(lse), _p(acc),
-        0 if acc is None else acc.shape[1], _p(buf), nbytes, _stream(stream)))
+        qp, pp, num_pages, page_size, tp, max_pages, np_, ip, T, L, P, H_q, H_kv, d, code,
+        d ** -0.5 if scale is None else scale, k_scale, v_scale, _ready(out, "out", q.dtype, cur),
+        _ready(lse, "lse", torch.float32, cur), ap, 0 if acc is None else acc.shape[1],
+        _scratch(ws, q, cur, nbytes, stream, h) if nbytes else None, nbytes, h))
     return out, lse
 
 
@@ -943,20 +993,15 @@ def misa_evict_select(acc, n, keep: int, sink: int = 0, recent: int = 0, L: Opti
         raise ValueError(f"acc must be [T, ld], got {tuple(acc.shape)}")
     T, ld = acc.shape
     L = ld if L is None else L
-    if n.dim() != 1 or n.shape[0] < T:
-        raise ValueError(f"n must be [>= {T}], got {tuple(n.shape)}")
+    _lengths(n, T)
     if idx is not None:
         _matrix(idx, "idx", T, keep)
     if n_out is not None and (n_out.dim() != 1 or n_out.shape[0] < T):
         raise ValueError(f"n_out must be [>= {T}], got {tuple(n_out.shape)}")
     if acc_out is not None:
         _matrix(acc_out, "acc_out", T, min_cols=keep)
-    _need(acc, "acc", torch.float32)
-    _need(n, "n", torch.int32)
-    _need_opt(idx, "idx", torch.int32)
-    _need_opt(n_out, "n_out", torch.int32)
-    _need_opt(acc_out, "acc_out", torch.float32)
-    _on_device(acc, n, idx, n_out, acc_out)
+    cur = _current(acc, "acc")
+    ap, np_ = _ready(acc, "acc", torch.float32, cur), _ready(n, "n", torch.int32, cur)
     if idx is None:
         idx = torch.empty((T, keep), dtype=torch.int32, device=acc.device)
     if n_out is None:
@@ -964,8 +1009,9 @@ def misa_evict_select(acc, n, keep: int, sink: int = 0, recent: int = 0, L: Opti
     if acc_out is None and want_acc:
         acc_out = torch.empty((T, keep), dtype=torch.float32, device=acc.device)
     _check("misa_evict_select", _lib.misa_evict_select(
-        _p(acc), ld, _p(n), T, L, keep, sink, recent, _p(idx), _p(n_out), _p(acc_out),
-        0 if acc_out is None else acc_out.shape[1], _stream(stream)))
+        ap, ld, np_, T, L, keep, sink, recent, _ready(idx, "idx", torch.int32, cur),
+        _ready(n_out, "n_out", torch.int32, cur), _ready(acc_out, "acc_out", torch.float32, cur),
+        0 if acc_out is None else acc_out.shape[1], _handle(stream, cur)))
     return idx, n_out, acc_out
 
 
@@ -976,15 +1022,13 @@ def misa_kv4_compact(pool, page_table, idx, d: int, ws: Optional[Workspace] = No
         raise ValueError(f"idx must be [T, keep], got {tuple(idx.shape)}")
     T, keep = idx.shape
     num_pages, H_kv, page_size, max_pages = _kv4_geometry(pool, page_table, T, d)
-    _need(pool, "pool", torch.uint8)
-    _need(page_table, "page_table", torch.int32)
-    _need(idx, "idx", torch.int32)
-    _on_device(pool, page_table, idx)
-    nbytes = misa_workspace_bytes(OP_KV4_COMPACT, T, 0, H_kv, 0, d, keep)
-    buf = _ws(ws, pool.device, stream).get(nbytes, stream)
+    cur = _current(pool, "pool")
+    pp, tp = _ready(pool, "pool", torch.uint8, cur), _ready(page_table, "page_table", torch.int32, cur)
+    ip, h = _ready(idx, "idx", torch.int32, cur), _handle(stream, cur)
+    nbytes = _ws_bytes(OP_KV4_COMPACT, T, 0, H_kv, 0, d, keep, 0)
     _check("misa_kv4_compact", _lib.misa_kv4_compact(
-        _p(pool), num_pages, page_size, _p(page_table), max_pages, _p(idx), T, keep, H_kv, d, _p(buf), nbytes,
-        _stream(stream)))
+        pp, num_pages, page_size, tp, max_pages, ip, T, keep, H_kv, d,
+        _scratch(ws, pool, cur, nbytes, stream, h) if nbytes else None, nbytes, h))
 
 
 def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = None, stream=None) -> None:
@@ -996,16 +1040,15 @@ def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = Non
         raise ValueError(f"idx must be [T, keep], got {tuple(idx.shape)}")
     T, keep = idx.shape
     _matrix(page_table, "page_table", T)
-    _need(pool, "pool")
-    _need(page_table, "page_table", torch.int32)
-    _need(idx, "idx", torch.int32)
-    _on_device(pool, page_table, idx)
+    cur = _current(pool, "pool")
+    code = _dtype_code(pool)
+    pp, tp = _ready(pool, "pool", pool.dtype, cur), _ready(page_table, "page_table", torch.int32, cur)
+    ip, h = _ready(idx, "idx", torch.int32, cur), _handle(stream, cur)
     num_pages, page_size, d = pool.shape
-    nbytes = misa_workspace_bytes(OP_KEYS_COMPACT_PAGED, T, 0, 0, 0, d * pool.element_size(), keep)
-    buf = _ws(ws, pool.device, stream).get(nbytes, stream)
+    nbytes = _ws_bytes(OP_KEYS_COMPACT_PAGED, T, 0, 0, 0, d * pool.element_size(), keep, 0)
     _check("misa_keys_compact_paged", _lib.misa_keys_compact_paged(
-        _p(pool), num_pages, page_size, _p(page_table), page_table.shape[1], _p(idx), T, keep, d, _dtype_code(pool),
-        _p(buf), nbytes, _stream(stream)))
+        pp, num_pages, page_size, tp, page_table.shape[1], ip, T, keep, d, code,
+        _scratch(ws, pool, cur, nbytes, stream, h) if nbytes else None, nbytes, h))
 
 
 def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, lse=None,
@@ -1015,7 +1058,7 @@ def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = Non
     being its last tokens -> (out [Tq, H_q, d], lse [Tq, H_q] or None).  scale defaults to 1 / sqrt(d).
     Rows of q, k and v may be strided (views of a fused projection); rows of given out and lse outside
     the sequences are left as they are."""
-    ldq, ldk, ldv = (_packed_rows(t, name, torch.bfloat16) for t, name in ((q, "q"), (k, "k"), (v, "v")))
+    ldq, ldk, ldv = _packed_rows(q, "q"), _packed_rows(k, "k"), _packed_rows(v, "v")
     Tq, H_q, d = q.shape
     Tk, H_kv, dk = k.shape
     if k.shape != v.shape or dk != d:
@@ -1028,16 +1071,14 @@ def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = Non
         raise ValueError(f"out must be {[Tq, H_q, d]}, got {tuple(out.shape)}")
     if lse is not None and tuple(lse.shape) != (Tq, H_q):
         raise ValueError(f"lse must be {[Tq, H_q]}, got {tuple(lse.shape)}")
-    _need(cu_q, "cu_q", torch.int32)
-    _need(cu_k, "cu_k", torch.int32)
-    _need_opt(out, "out", torch.bfloat16)
-    _need_opt(lse, "lse", torch.float32)
-    _on_device(q, k, v, cu_q, cu_k, out, lse)
+    cur, bf = _current(q, "q"), torch.bfloat16
+    qp, kp, vp = _rows_ready(q, "q", bf, cur), _rows_ready(k, "k", bf, cur), _rows_ready(v, "v", bf, cur)
+    cq, ck = _ready(cu_q, "cu_q", torch.int32, cur), _ready(cu_k, "cu_k", torch.int32, cur)
     if out is None:
-        out = torch.empty((Tq, H_q, d), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((Tq, H_q, d), dtype=bf, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty((Tq, H_q), dtype=torch.float32, device=q.device)
     _check("misa_prompt_attention", _lib.misa_prompt_attention(
-        _p(q), _p(k), _p(v), ldq, ldk, ldv, _p(cu_q), _p(cu_k), S, Tq, Tk, H_q, H_kv, d, BF16,
-        d ** -0.5 if scale is None else scale, _p(out), _p(lse), _stream(stream)))
+        qp, kp, vp, ldq, ldk, ldv, cq, ck, S, Tq, Tk, H_q, H_kv, d, BF16, d ** -0.5 if scale is None else scale,
+        _ready(out, "out", bf, cur), _ready(lse, "lse", torch.float32, cur), _handle(stream, cur)))
     return out, lse

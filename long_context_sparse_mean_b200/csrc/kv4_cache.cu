@@ -182,11 +182,13 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Pool pool, const int32
 // Rows that stay where they are are passed over, and so are rows whose own or source page is not in the
 // pool.  Bound by HBM: rows are read and written once.
 // Waits are bounded (1 s); a segment whose wait runs out is not written and a status word is set.
-constexpr int kSeg = 64;                // rows of a segment where there are several
+constexpr int kSeg = 64;                // fewest rows of a segment where there are several
+constexpr int kGpuSms = 148;
 constexpr int kGroupBytes = 72 * 1024;  // its rows in shared memory: three CTAs an SM
 constexpr int kOneSeg = 512;            // longest list taken as one segment,
 constexpr int kOneSegBytes = 160 * 1024;  // where a slab's rows of it fit here
 constexpr int kFewCtas = 96;
+constexpr int kCompactThreads = 512;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
 __device__ int g_compact_status = 0;
@@ -216,23 +218,26 @@ __device__ __forceinline__ int first_at_least(const int32_t* list, int count, in
   return lo;
 }
 
-template <int P>  // 16-byte pieces of a row
-__global__ void __launch_bounds__(256) compact_rows_kernel(RowPages pages, int slabs, int group, int64_t slab_bytes,
-                                                           int sb, const int32_t* __restrict__ idx, int keep, int R,
-                                                           uint32_t* __restrict__ read_marks) {
+// Slabs are `stride` bytes apart inside a page, their code rows row_bytes; a CTA moves 16 P bytes of a row of
+// each slab of its group, and behind scales_at bytes of a slab its scale rows of sb bytes (0: none).
+template <int P>
+__global__ void __launch_bounds__(kCompactThreads) compact_rows_kernel(RowPages pages, int slabs, int group,
+                                                                       int64_t stride, int row_bytes, int64_t page_bytes,
+                                                                       int64_t scales_at, int sb,
+                                                                       const int32_t* __restrict__ idx, int keep, int R,
+                                                                       uint32_t* __restrict__ read_marks) {
+  constexpr int rb = 16 * P;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int first_wait, end_wait, late;
   const int seg = blockIdx.x, t = blockIdx.z, s0 = blockIdx.y * group, ns = min(group, slabs - s0);
   const int j0 = seg * R, warp = threadIdx.x >> 5;
-  constexpr int rb = 16 * P;
   const int32_t* list = idx + (int64_t)t * keep;
-  const int64_t page_bytes = (int64_t)slabs * slab_bytes, scales_at = (int64_t)pages.page_size * rb;
   uint32_t* marks = read_marks + ((int64_t)t * gridDim.y + blockIdx.y) * gridDim.x;
   uint8_t* const rows = smem;                                // [slab][row][rb]
   uint8_t* const sc = rows + (int64_t)ns * R * rb;           // [slab][row][sb]
   int4* const place = reinterpret_cast<int4*>(smem + (int64_t)group * R * (rb + sb));  // source page, slot; own page, slot
   bool any = false;
-  for (int r = threadIdx.x; r < R; r += 256) {
+  for (int r = threadIdx.x; r < R; r += kCompactThreads) {
     const int j = j0 + r, src = j < keep ? __ldg(list + j) : -1;
     int64_t pf = -1, pt = -1;
     if (src >= 0 && src != j) {
@@ -246,22 +251,23 @@ __global__ void __launch_bounds__(256) compact_rows_kernel(RowPages pages, int s
   }
   if (threadIdx.x == 0) late = 0;
   const bool moves = __syncthreads_or(any);
-  uint8_t* const base = pages.base + s0 * slab_bytes;
+  uint8_t* const base = pages.base + s0 * stride;
+  const int each = ns >= 8 ? 8 : 1;  // threads that share a row's scales
   if (moves) {
-    for (int u = threadIdx.x; u < R * P; u += 256) {
+    for (int u = threadIdx.x; u < R * P; u += kCompactThreads) {
       const int r = u / P, piece = u % P;
       const int4 w = place[r];
       if (w.x < 0) continue;
-      const uint8_t* p = base + w.x * page_bytes + (int64_t)w.y * rb + piece * 16;
-      for (int x = 0; x < ns; ++x) copy16_async(rows + ((int64_t)x * R + r) * rb + piece * 16, p + x * slab_bytes);
+      const uint8_t* p = base + w.x * page_bytes + (int64_t)w.y * row_bytes + piece * 16;
+      for (int x = 0; x < ns; ++x) copy16_async(rows + ((int64_t)x * R + r) * rb + piece * 16, p + x * stride);
     }
     if (sb) {
-      for (int u = threadIdx.x; u < R * 8; u += 256) {  // eight threads a row, each every eighth slab
-        const int r = u >> 3;
+      for (int u = threadIdx.x; u < R * each; u += kCompactThreads) {
+        const int r = u / each;
         const int4 w = place[r];
         if (w.x < 0) continue;
-        for (int x = u & 7; x < ns; x += 8) {
-          const uint8_t* p = base + w.x * page_bytes + x * slab_bytes + scales_at + (int64_t)w.y * sb;
+        for (int x = u % each; x < ns; x += each) {
+          const uint8_t* p = base + w.x * page_bytes + x * stride + scales_at + (int64_t)w.y * sb;
           const uint32_t q = (uint32_t)__cvta_generic_to_shared(sc + ((int64_t)x * R + r) * sb);
           if (sb == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(q), "l"(p) : "memory");
           else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(q), "l"(p) : "memory");
@@ -304,22 +310,22 @@ __global__ void __launch_bounds__(256) compact_rows_kernel(RowPages pages, int s
       return;
     }
   }
-  for (int u = threadIdx.x; u < R * P; u += 256) {
+  for (int u = threadIdx.x; u < R * P; u += kCompactThreads) {
     const int r = u / P, piece = u % P;
     const int4 w = place[r];
     if (w.x < 0) continue;
-    uint8_t* p = base + w.z * page_bytes + (int64_t)w.w * rb + piece * 16;
+    uint8_t* p = base + w.z * page_bytes + (int64_t)w.w * row_bytes + piece * 16;
 #pragma unroll 4
     for (int x = 0; x < ns; ++x)
-      *reinterpret_cast<uint4*>(p + x * slab_bytes) = *reinterpret_cast<const uint4*>(rows + ((int64_t)x * R + r) * rb + piece * 16);
+      *reinterpret_cast<uint4*>(p + x * stride) = *reinterpret_cast<const uint4*>(rows + ((int64_t)x * R + r) * rb + piece * 16);
   }
   if (sb) {
-    for (int u = threadIdx.x; u < R * 8; u += 256) {
-      const int r = u >> 3;
+    for (int u = threadIdx.x; u < R * each; u += kCompactThreads) {
+      const int r = u / each;
       const int4 w = place[r];
       if (w.x < 0) continue;
-      for (int x = u & 7; x < ns; x += 8) {
-        uint8_t* p = base + w.z * page_bytes + x * slab_bytes + scales_at + (int64_t)w.w * sb;
+      for (int x = u % each; x < ns; x += each) {
+        uint8_t* p = base + w.z * page_bytes + x * stride + scales_at + (int64_t)w.w * sb;
         const uint8_t* q = sc + ((int64_t)x * R + r) * sb;
         if (sb == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(q);
         else *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(q);
@@ -338,7 +344,9 @@ CompactPlan compact_plan(int T, int slabs, int rb, int sb, int keep) {
   CompactPlan p;
   const int row = rb + sb;
   int64_t room = kGroupBytes;
-  p.R = kSeg;
+  // rows that fill the room, unless that leaves CTAs without any
+  const int64_t fill = room / ((int64_t)slabs * row), share = (int64_t)T * keep / (4 * kGpuSms);
+  p.R = (int)std::max<int64_t>(kSeg, std::min(std::min<int64_t>(fill, share) / 16 * 16, (int64_t)kOneSeg));
   if (keep <= kOneSeg && (int64_t)keep * row <= kOneSegBytes) {
     p.R = (keep + 15) / 16 * 16;
     room = std::max<int64_t>(room, (int64_t)p.R * row);
@@ -372,16 +380,22 @@ void launch_kv4_read(DType dt, const Kv4Pool& pool, const int32_t* cu, const int
   else dt == DType::BF16 ? run(kv4_read_kernel<64, DType::BF16>) : run(kv4_read_kernel<64, DType::F32>);
 }
 
-size_t compact_ws_bytes(int T, int keep, int slabs, int rb, int sb) {
+size_t compact_ws_bytes(int T, int keep, int slabs, int row, int sb) {
+  const int rb = sb ? row : 64;
+  slabs *= row / rb;
   const CompactPlan p = compact_plan(T, slabs, rb, sb, keep);
   return sizeof(uint32_t) * (size_t)T * p.groups * p.segs;
 }
 
-bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, int rb, int sb, const int32_t* idx,
+bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, int row, int sb, const int32_t* idx,
                          int T, int keep, void* ws, cudaStream_t s) {
   if (T <= 0 || keep <= 0) return true;
+  // a wide row without scales goes in columns of 64 bytes, as slabs of their own
+  const int64_t page_bytes = slabs * slab_bytes, stride = sb ? slab_bytes : 64, scales_at = (int64_t)pages.page_size * row;
+  const int rb = sb ? row : 64;
+  slabs *= row / rb;
   const CompactPlan p = compact_plan(T, slabs, rb, sb, keep);
-  if (p.segs > 1 && cudaMemsetAsync(ws, 0, compact_ws_bytes(T, keep, slabs, rb, sb), s) != cudaSuccess) return false;
+  if (p.segs > 1 && cudaMemsetAsync(ws, 0, sizeof(uint32_t) * (size_t)T * p.groups * p.segs, s) != cudaSuccess) return false;
   auto run = [&](auto kernel) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOneSegBytes + 16384) != cudaSuccess)
       return false;
@@ -389,24 +403,13 @@ bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, i
     for (int t0 = 0; t0 < T; t0 += kMostZ) {
       RowPages q = pages;
       q.table += (int64_t)t0 * pages.max_pages;
-      kernel<<<dim3(p.segs, p.groups, std::min(T - t0, kMostZ)), 256, p.smem, s>>>(
-          q, slabs, p.group, slab_bytes, sb, idx + (int64_t)t0 * keep, keep, p.R,
+      kernel<<<dim3(p.segs, p.groups, std::min(T - t0, kMostZ)), kCompactThreads, p.smem, s>>>(
+          q, slabs, p.group, stride, row, page_bytes, scales_at, sb, idx + (int64_t)t0 * keep, keep, p.R,
           static_cast<uint32_t*>(ws) + (int64_t)t0 * p.groups * p.segs);
     }
     return true;
   };
-  switch (rb) {
-    case 32:
-      return run(compact_rows_kernel<2>);
-    case 64:
-      return run(compact_rows_kernel<4>);
-    case 256:
-      return run(compact_rows_kernel<16>);
-    case 512:
-      return run(compact_rows_kernel<32>);
-    default:
-      return false;
-  }
+  return rb == 32 ? run(compact_rows_kernel<2>) : run(compact_rows_kernel<4>);
 }
 
 int read_and_clear_compact_status() {
