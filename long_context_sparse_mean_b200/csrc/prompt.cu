@@ -94,15 +94,71 @@ struct Item {
   }
 };
 
+// Waits for the barrier phase with this parity; false once *abort is set or after the time limit.  The
+// clock and the abort word are looked at every 256 tries only: reading the clock takes about as long
+// as a piece of the softmax.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  uint64_t t0 = 0;
+  for (uint32_t spin = 1;; ++spin) {
+    if (tc::mbar_test(bar, parity)) return true;
+    if ((spin & 255u) == 0) {
+      if (abort && *abort) return false;
+      const uint64_t now = tc::global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) return false;
+    }
+  }
+}
+
+// The same with a test that never suspends the thread, for the one thread all others wait for.
+__device__ __forceinline__ bool spin_for(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  uint64_t t0 = 0;
+  for (uint32_t spin = 1;; ++spin) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((spin & 1023u) == 0) {
+      if (abort && *abort) return false;
+      const uint64_t now = tc::global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) return false;
+    }
+  }
+}
+
 __device__ __forceinline__ void give_up(volatile int* abort) {
   *abort = 1;
   atomicExch(&g_prompt_status, 1);
+}
+
+// True in one thread of the warp, chosen so that the compiler knows there is only one (tensor-core and bulk
+// copy instructions take warp-uniform operands; under a test of the lane number it loops over lanes).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
 }
 
 // Shared-memory descriptor of V [keys][64 dims] boxes as the B operand with dims contiguous: 64-element
@@ -120,6 +176,23 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Scores from position `seen` on become minus infinity.
+__device__ __forceinline__ void hide(uint32_t (&s)[32], int seen) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (e >= seen) s[e] = 0xff800000u;
+}
+
+// Warp-wide: lane l writes 16 consecutive columns of TMEM lane (taddr.lane + l).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 
@@ -248,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.f;  // maximum of the raw scores, sum of the weights
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      if (!tc::mbar_wait(sfull(t), j & 1, abort, kWaitLimitNs)) {
+      if (!wait_for(sfull(t), j & 1, abort)) {
         ok = false;
         break;
       }
@@ -261,25 +334,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.masked(t, j)) {
         const int seen = min(it.keys, i + it.off + 1) - j * kRows;  // keys of this block that row i sees
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (32 * x + e >= seen) s[x][e] = 0xff800000u;
+        for (int x = 0; x < 4; ++x) hide(s[x], seen - 32 * x);
       }
       float top[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        top[x] = __uint_as_float(s[x][0]);
+      for (int x = 0; x < 4; ++x) top[x] = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
 #pragma unroll
-        for (int e = 1; e < 31; e += 2)
-          top[x] = fmaxf(fmaxf(top[x], __uint_as_float(s[x][e])), __uint_as_float(s[x][e + 1]));
-        top[x] = fmaxf(top[x], __uint_as_float(s[x][31]));
-      }
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      for (int e = 2; e < 32; e += 2)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top[x] = max3(top[x], __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
+      const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
       const bool raise = mx * c > m * c + kSlack;  // also the first score that is seen
       if (__any_sync(0xffffffffu, raise && j > 0)) {
         // O holds blocks 0 .. j - 1 once their product is through
-        if (!tc::mbar_wait(odone(t), (j - 1) & 1, abort, kWaitLimitNs)) {
+        if (!wait_for(odone(t), (j - 1) & 1, abort)) {
           ok = false;
           break;
         }
@@ -298,29 +366,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (raise) m = mx;
       const float neg = m == -INFINITY ? 0.f : -m * c;
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      // Weights go pair by pair through multiply-add, exponential, and kLag pairs later sum and rounding, so
+      // that the exponentials (8 clocks a warp and instruction) never wait for their own results; 16 pairs
+      // are written at a time, over scores that have been read.
+      constexpr int kLag = 6;
+      float2 sum[4];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        uint32_t p[32];
+      for (int x = 0; x < 4; ++x) sum[x] = make_float2(0.f, 0.f);
+      float2 w[kLag];
+      uint32_t p[2][16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const uint32_t* src = s[2 * x + e / 16];
-          const float2 z = __ffma2_rn(make_float2(__uint_as_float(src[2 * (e % 16)]), __uint_as_float(src[2 * (e % 16) + 1])),
-                                      make_float2(c, c), make_float2(neg, neg));
-          const float2 w = make_float2(ex2(z.x), ex2(z.y));
-          sum[e & 1] = __fadd2_rn(sum[e & 1], w);
-          const __nv_bfloat162 h = __floats2bfloat162_rn(w.x, w.y);
-          p[e] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int e = 0; e < 64 + kLag; ++e) {
+        if (e >= kLag) {
+          const int y = e - kLag;
+          const float2 v = w[y % kLag];
+          sum[y & 3] = __fadd2_rn(sum[y & 3], v);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+          p[(y >> 4) & 1][y & 15] = *reinterpret_cast<const uint32_t*>(&h);
+          if ((y & 15) == 15) tmem_st16(ts + y - 15, p[(y >> 4) & 1]);
         }
-        tmem_st32(ts + 32 * x, p);
+        if (e < 64) {
+          const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[e / 16][2 * (e % 16)]), __uint_as_float(s[e / 16][2 * (e % 16) + 1])),
+                                      make_float2(c, c), make_float2(neg, neg));
+          w[e % kLag] = make_float2(ex2(z.x), ex2(z.y));
+        }
       }
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
       tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(pfull(t));
+      if (lane == 0) tc::mbar_arrive_relaxed(pfull(t));  // what it hands on lies in tensor memory
     }
-    if (ok && n > 0 && !tc::mbar_wait(odone(t), (n - 1) & 1, abort, kWaitLimitNs)) ok = false;
+    if (ok && n > 0 && !wait_for(odone(t), (n - 1) & 1, abort)) ok = false;
     tc::tc_fence_after();
     if (!ok) give_up(abort);
     if (ok && t * kRows < it.rows) {
@@ -385,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kLoadWarp) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       const int hk = it.head / a.G;
       bool ok = true;
       uint32_t u = 0;
@@ -400,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; ok && j < nblk; ++j) {
         for (int side = 0; side < 2; ++side, ++u) {
           const int b = u % NB;
-          if (u >= NB && !tc::mbar_wait(empty(b), ((u / NB) - 1) & 1, abort, kWaitLimitNs)) {
+          if (u >= NB && !wait_for(empty(b), ((u / NB) - 1) & 1, abort)) {
             ok = false;
             break;
           }
@@ -414,19 +491,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) give_up(abort);
       // every issued copy lands before the CTA exits
-      if (nA > 0) tc::mbar_wait(qfull(0), 0, nullptr, kWaitLimitNs);
-      if (nB > 0) tc::mbar_wait(qfull(1), 0, nullptr, kWaitLimitNs);
-      for (uint32_t g = u > NB ? u - NB : 0; g < u; ++g) tc::mbar_wait(full(g % NB), (g / NB) & 1, nullptr, kWaitLimitNs);
+      if (nA > 0) wait_for(qfull(0), 0, nullptr);
+      if (nB > 0) wait_for(qfull(1), 0, nullptr);
+      for (uint32_t g = u > NB ? u - NB : 0; g < u; ++g) wait_for(full(g % NB), (g / NB) & 1, nullptr);
     }
   } else if (warp == kMmaWarp) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc_s = tc::idesc_bf16_f32(kRows, kRows);
       constexpr uint32_t idesc_o = tc::idesc_bf16_f32(kRows, D) | (1u << 16);  // V with its dims contiguous
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok && !tc::mbar_wait(bar, parity, abort, kWaitLimitNs)) ok = false;
-        tc::tc_fence_after();
+        if (ok && !spin_for(bar, parity, abort)) ok = false;
         return ok;
       };
       auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
@@ -444,8 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto values = [&](int t, int j) {  // O_t += P_t V_j
         const uint32_t u = 2 * j + 1, b = u % NB;
-        if (!wait(pfull(t), j & 1)) return;
         if (!wait(vok(b), (u / NB) & 1)) return;
+        if (!wait(pfull(t), j & 1)) return;
+        tc::tc_fence_after();  // after the weights' stores to tensor memory, by other threads
 #pragma unroll
         for (int kk = 0; kk < kRows / 16; ++kk)
           mma_bf16_ts(tmem + 2 * kRows + t * kRows, tmem + t * kRows + kk * 8,
@@ -466,14 +543,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) give_up(abort);
       // every issued MMA completes before tensor memory is freed
       tc::mma_commit(drain);
-      tc::mbar_wait(drain, 0, nullptr, kWaitLimitNs);
+      wait_for(drain, 0, nullptr);
     }
   } else {
     // ---------------- guards ----------------
     bool ok = true;
     for (int j = 0; ok && j < nblk; ++j) {
       const uint32_t u = 2 * j + 1, b = u % NB;
-      if (!tc::mbar_wait(full(b), (u / NB) & 1, abort, kWaitLimitNs)) {
+      if (!wait_for(full(b), (u / NB) & 1, abort)) {
         ok = false;
         break;
       }
