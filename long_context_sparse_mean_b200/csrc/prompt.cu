@@ -51,6 +51,7 @@ static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= 168 * kThreads, "register
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kGuardWarp = 10;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s
+constexpr int kLag = 6;                     // pairs of weights between their exponentials and their sum
 constexpr float kSlack = 8.f;               // base-2 growth of a row's scores before its maximum is raised
 
 template <int D>
@@ -61,7 +62,7 @@ struct Lay {
   static constexpr int kOffQ = 0;
   static constexpr int kOffRing = 2 * kTileBytes;
   static constexpr int kOffBar = kOffRing + kBufs * kTileBytes;
-  static constexpr int kNumBars = 2 + 3 * kBufs + 6 + 1;
+  static constexpr int kNumBars = 2 + 3 * kBufs + 8 + 1;
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 256 + 1024;      // + alignment slack
 };
@@ -102,28 +103,6 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, const vo
   for (uint32_t spin = 1;; ++spin) {
     if (tc::mbar_test(bar, parity)) return true;
     if ((spin & 255u) == 0) {
-      if (abort && *abort) return false;
-      const uint64_t now = tc::global_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kWaitLimitNs) return false;
-    }
-  }
-}
-
-// The same with a test that never suspends the thread, for the one thread all others wait for.
-__device__ __forceinline__ bool spin_for(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  uint64_t t0 = 0;
-  for (uint32_t spin = 1;; ++spin) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if ((spin & 1023u) == 0) {
       if (abort && *abort) return false;
       const uint64_t now = tc::global_ns();
       if (t0 == 0) t0 = now;
@@ -280,12 +259,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto sfull = [&](int t) { return bar0 + 8 * (2 + 3 * NB + t); };
   auto pfull = [&](int t) { return bar0 + 8 * (4 + 3 * NB + t); };
   auto odone = [&](int t) { return bar0 + 8 * (6 + 3 * NB + t); };
-  const uint32_t drain = bar0 + 8 * (8 + 3 * NB);
+  auto phalf = [&](int t) { return bar0 + 8 * (8 + 3 * NB + t); };
+  const uint32_t drain = bar0 + 8 * (10 + 3 * NB);
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(qfull(t), 1);
       tc::mbar_init(sfull(t), 1);
       tc::mbar_init(pfull(t), 4);
+      tc::mbar_init(phalf(t), 4);
       tc::mbar_init(odone(t), 1);
     }
     for (int i = 0; i < NB; ++i) {
@@ -336,62 +317,86 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x) hide(s[x], seen - 32 * x);
       }
-      float top[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) top[x] = fmaxf(__uint_as_float(s[x][0]), __uint_as_float(s[x][1]));
-#pragma unroll
-      for (int e = 2; e < 32; e += 2)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) top[x] = max3(top[x], __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
-      const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-      const bool raise = mx * c > m * c + kSlack;  // also the first score that is seen
-      if (__any_sync(0xffffffffu, raise && j > 0)) {
-        // O holds blocks 0 .. j - 1 once their product is through
-        if (!wait_for(odone(t), (j - 1) & 1, abort)) {
-          ok = false;
-          break;
-        }
-        tc::tc_fence_after();
-        const float f = raise && m != -INFINITY ? ex2((m - mx) * c) : 1.f;
-        l *= f;
-#pragma unroll 1
-        for (int x = 0; x < D / 32; ++x) {
-          uint32_t o[32];
-          tc::tmem_ld32(to + 32 * x, o);
-          tc::tmem_ld_wait(o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tmem_st32(to + 32 * x, o);
-        }
-      }
-      if (raise) m = mx;
-      const float neg = m == -INFINITY ? 0.f : -m * c;
       // Weights go pair by pair through multiply-add, exponential, and kLag pairs later sum and rounding, so
       // that the exponentials (8 clocks a warp and instruction) never wait for their own results; 16 pairs
-      // are written at a time, over scores that have been read.
-      constexpr int kLag = 6;
-      float2 sum[4];
+      // are written at a time, over scores that have been read.  They start from the running maximum as it
+      // is, while the block's own maximum is found among the first 16 pairs' exponentials; should that pass
+      // it, these pairs are done again.
+      float2 sum[2], w[kLag];
+      uint32_t p[16];
+      float neg = m == -INFINITY ? 0.f : -m * c;
+      sum[0] = sum[1] = make_float2(0.f, 0.f);
+      auto start = [&](int e) {  // exponentials of pair e
+        const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[e / 16][2 * (e % 16)]), __uint_as_float(s[e / 16][2 * (e % 16) + 1])),
+                                    make_float2(c, c), make_float2(neg, neg));
+        w[e % kLag] = make_float2(ex2(z.x), ex2(z.y));
+      };
+      auto finish = [&](int e) {  // its sum and its rounding
+        const float2 v = w[e % kLag];
+        sum[e & 1] = __fadd2_rn(sum[e & 1], v);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+        p[e & 15] = *reinterpret_cast<const uint32_t*>(&h);
+      };
+      float top[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) sum[x] = make_float2(0.f, 0.f);
-      float2 w[kLag];
-      uint32_t p[2][16];
+      for (int x = 0; x < 4; ++x) top[x] = __uint_as_float(s[x][0]);
 #pragma unroll
-      for (int e = 0; e < 64 + kLag; ++e) {
-        if (e >= kLag) {
-          const int y = e - kLag;
-          const float2 v = w[y % kLag];
-          sum[y & 3] = __fadd2_rn(sum[y & 3], v);
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-          p[(y >> 4) & 1][y & 15] = *reinterpret_cast<const uint32_t*>(&h);
-          if ((y & 15) == 15) tmem_st16(ts + y - 15, p[(y >> 4) & 1]);
-        }
-        if (e < 64) {
-          const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[e / 16][2 * (e % 16)]), __uint_as_float(s[e / 16][2 * (e % 16) + 1])),
-                                      make_float2(c, c), make_float2(neg, neg));
-          w[e % kLag] = make_float2(ex2(z.x), ex2(z.y));
+      for (int e = 0; e < 16 + kLag; ++e) {
+        if (e >= kLag) finish(e - kLag);
+        if (e < 16) {
+          start(e);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) top[x] = max3(top[x], __uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1]));
         }
       }
-      l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) + ((sum[2].x + sum[2].y) + (sum[3].x + sum[3].y));
+      const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+      const bool raise = mx * c > m * c + kSlack;  // also the first score that is seen
+      if (__any_sync(0xffffffffu, raise)) {
+        if (j > 0) {
+          // O holds blocks 0 .. j - 1 once their product is through
+          if (!wait_for(odone(t), (j - 1) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const float f = raise && m != -INFINITY ? ex2((m - mx) * c) : 1.f;
+          l *= f;
+#pragma unroll 1
+          for (int x = 0; x < D / 32; ++x) {
+            uint32_t o[32];
+            tc::tmem_ld32(to + 32 * x, o);
+            tc::tmem_ld_wait(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(to + 32 * x, o);
+          }
+        }
+        if (raise) m = mx;
+        neg = m == -INFINITY ? 0.f : -m * c;
+        sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 16 + kLag; ++e) {
+          if (e >= kLag) finish(e - kLag);
+          if (e < 16) start(e);
+        }
+      }
+      tmem_st16(ts, p);
+#pragma unroll
+      for (int e = 16; e < 64 + kLag; ++e) {
+        if (e >= 16 + kLag) {
+          const int y = e - kLag;
+          finish(y);
+          if ((y & 15) == 15) tmem_st16(ts + y - 15, p);
+          if (y == 31) {  // half of the weights are there: their product may start
+            tmem_st_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_relaxed(phalf(t));
+          }
+        }
+        if (e < 64) start(e);
+      }
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc_o = tc::idesc_bf16_f32(kRows, D) | (1u << 16);  // V with its dims contiguous
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok && !spin_for(bar, parity, abort)) ok = false;
+        if (ok && !wait_for(bar, parity, abort)) ok = false;
         return ok;
       };
       auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
@@ -521,13 +526,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto values = [&](int t, int j) {  // O_t += P_t V_j
         const uint32_t u = 2 * j + 1, b = u % NB;
         if (!wait(vok(b), (u / NB) & 1)) return;
-        if (!wait(pfull(t), j & 1)) return;
-        tc::tc_fence_after();  // after the weights' stores to tensor memory, by other threads
 #pragma unroll
-        for (int kk = 0; kk < kRows / 16; ++kk)
-          mma_bf16_ts(tmem + 2 * kRows + t * kRows, tmem + t * kRows + kk * 8,
-                      sw128_mnmajor_desc(ring + b * L::kTileBytes + kk * 2048, L::kHalfBytes), idesc_o,
-                      (j | kk) != 0);
+        for (int half = 0; half < 2; ++half) {
+          if (!wait(half ? pfull(t) : phalf(t), j & 1)) return;
+          tc::tc_fence_after();  // after the weights' stores to tensor memory, by other threads
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            mma_bf16_ts(tmem + 2 * kRows + t * kRows, tmem + t * kRows + kk * 8,
+                        sw128_mnmajor_desc(ring + b * L::kTileBytes + kk * 2048, L::kHalfBytes), idesc_o,
+                        (j | kk) != 0);
+        }
         tc::mma_commit(odone(t));
         if (t == 1 || j >= nB) tc::mma_commit(empty(b));
       };
