@@ -81,7 +81,8 @@ typedef enum {
   MISA_OP_HIER_FUSED = 10,
   MISA_OP_KV4_ATTENTION = 11,
   MISA_OP_KV4_COMPACT = 12,
-  MISA_OP_KEYS_COMPACT_PAGED = 13
+  MISA_OP_KEYS_COMPACT_PAGED = 13,
+  MISA_OP_PROMPT_ATTENTION = 14
 } misa_op;
 
 /* Largest k' accepted by misa_hier_rerank (its candidates are ranked in shared memory). */
@@ -439,11 +440,15 @@ misa_status misa_keys_compact_paged(void* pool, int64_t num_pages, int page_size
  *   q      : [Tq][H_q][d] at row stride ldq elements; k, v : [Tk][H_kv][d] at ldk, ldv (multiples of 8
  *            elements, so the views of one fused projection serve; 16-byte aligned); bf16 only
  *   out    : [Tq][H_q][d] bf16;  lse_opt : [Tq][H_q] fp32, or NULL
- * Rows of other sequences never reach a sequence's outputs, whatever they hold.
+ * Rows of other sequences never reach a sequence's outputs, whatever they hold, nor do keys and values
+ * behind a query reach its own.
+ *   ws     : misa_workspace_bytes(MISA_OP_PROMPT_ATTENTION, Tq, Tk, H_q, S, d, 0, 0) bytes (0 for a call of
+ *            few short prompts; otherwise mostly the pieces of what is cut between CTAs, 40 MB at d = 128)
  */
 misa_status misa_prompt_attention(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
                                   const int32_t* cu_q, const int32_t* cu_k, int S, int Tq, int Tk, int H_q, int H_kv,
-                                  int d, int dtype, float scale, void* out, float* lse_opt, void* stream);
+                                  int d, int dtype, float scale, void* out, float* lse_opt, void* ws, size_t ws_bytes,
+                                  void* stream);
 
 /*
  * Device-side status of the calls made so far on the current device.  The tensor-core kernels

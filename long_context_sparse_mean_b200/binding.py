@@ -33,7 +33,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_TIMEOU
 BF16, F32 = 0, 1
 (OP_ROUTE, OP_SCORE_TOPK, OP_RERANK, OP_DENSE_TOPK, OP_TOPK_SELECT, OP_BLOCK_FILTER, OP_ROUTE_PAGED,
  OP_SCORE_TOPK_PAGED, OP_RERANK_PAGED, OP_SCORE_TOPK_FUSED, OP_HIER_FUSED,
- OP_KV4_ATTENTION, OP_KV4_COMPACT, OP_KEYS_COMPACT_PAGED) = range(14)
+ OP_KV4_ATTENTION, OP_KV4_COMPACT, OP_KEYS_COMPACT_PAGED, OP_PROMPT_ATTENTION) = range(15)
 MAX_KP = 16384
 
 if not os.path.exists(LIB_PATH):
@@ -80,8 +80,8 @@ def _setup(lib):
         "misa_evict_select": ([P, i64, P, i32, i32, i32, i32, i32, P, P, P, i64, P], i32),
         "misa_kv4_compact": ([P, i64, i32, P, i64, P, i32, i32, i32, i32, P, sz, P], i32),
         "misa_keys_compact_paged": ([P, i64, i32, P, i64, P, i32, i32, i32, i32, P, sz, P], i32),
-        "misa_prompt_attention": ([P, P, P, i64, i64, i64, P, P, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P],
-                                  i32),
+        "misa_prompt_attention": ([P, P, P, i64, i64, i64, P, P, i32, i32, i32, i32, i32, i32, i32, f32, P, P, P, sz,
+                                   P], i32),
     }
     for name, (args, res) in sigs.items():
         f = getattr(lib, name)
@@ -1052,7 +1052,7 @@ def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = Non
 
 
 def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, lse=None,
-                          want_lse: bool = False, stream=None):
+                          want_lse: bool = False, ws: Optional[Workspace] = None, stream=None):
     """Causal attention of packed prompts, q [Tq, H_q, d] and k, v [Tk, H_kv, d] in bf16: sequence b has
     queries cu_q[b] .. cu_q[b + 1] and keys cu_k[b] .. cu_k[b + 1] (cu_k defaults to cu_q), its queries
     being its last tokens -> (out [Tq, H_q, d], lse [Tq, H_q] or None).  scale defaults to 1 / sqrt(d).
@@ -1078,7 +1078,10 @@ def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = Non
         out = torch.empty((Tq, H_q, d), dtype=bf, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty((Tq, H_q), dtype=torch.float32, device=q.device)
+    h = _handle(stream, cur)
+    nbytes = _ws_bytes(OP_PROMPT_ATTENTION, Tq, Tk, H_q, S, d, 0, 0)
     _check("misa_prompt_attention", _lib.misa_prompt_attention(
         qp, kp, vp, ldq, ldk, ldv, cq, ck, S, Tq, Tk, H_q, H_kv, d, BF16, d ** -0.5 if scale is None else scale,
-        _ready(out, "out", bf, cur), _ready(lse, "lse", torch.float32, cur), _handle(stream, cur)))
+        _ready(out, "out", bf, cur), _ready(lse, "lse", torch.float32, cur),
+        _scratch(ws, q, cur, nbytes, stream, h) if nbytes else None, nbytes, h))
     return out, lse

@@ -212,6 +212,8 @@ size_t misa_workspace_bytes(int op, int T, int L, int H_I, int B, int h, int top
       return misa::kv4_attention_ws_bytes(T, topk > 0 ? topk : L, H_I, B, h, kp != 0);
     case MISA_OP_KV4_COMPACT:  // H_I kv heads, h head width, topk kept tokens
       return T > 0 && H_I > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, 2 * H_I, h / 2, h / 16) : 0;
+    case MISA_OP_PROMPT_ATTENTION:  // T queries, L keys, H_I query heads, B sequences, h head width
+      return H_I > 0 && h > 0 ? misa::prompt_ws_bytes(B, T, L, H_I, h) : 0;
     case MISA_OP_KEYS_COMPACT_PAGED:  // h bytes of a key row, topk kept tokens
       return T > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, 1, h, 0) : 0;
     default:

@@ -191,7 +191,8 @@ misa_status misa_keys_compact_paged(void* pool, int64_t num_pages, int page_size
 
 misa_status misa_prompt_attention(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
                                   const int32_t* cu_q, const int32_t* cu_k, int S, int Tq, int Tk, int H_q, int H_kv,
-                                  int d, int dtype, float scale, void* out, float* lse_opt, void* stream) {
+                                  int d, int dtype, float scale, void* out, float* lse_opt, void* ws, size_t ws_bytes,
+                                  void* stream) {
   if (S < 0 || Tq < 0 || Tk < 0 || H_q < 1 || H_kv < 1) return MISA_ERR_INVALID_ARG;
   if (dtype != MISA_BF16) return MISA_ERR_UNSUPPORTED;
   if (d != 64 && d != 128) return MISA_ERR_UNSUPPORTED;
@@ -203,7 +204,9 @@ misa_status misa_prompt_attention(const void* q, const void* k, const void* v, i
   if (st == MISA_OK && Tk > 0) st = check_rows(k, ldk, H_kv, d, dtype);
   if (st == MISA_OK && Tk > 0) st = check_rows(v, ldv, H_kv, d, dtype);
   if (st != MISA_OK) return st;
-  if (!misa::launch_prompt_attention(q, k, v, ldq, ldk, ldv, cu_q, cu_k, S, Tq, Tk, H_q, H_kv, d, scale, out, lse_opt,
+  const size_t need = misa::prompt_ws_bytes(S, Tq, Tk, H_q, d);
+  if (need > 0 && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255))) return MISA_ERR_WORKSPACE;
+  if (!misa::launch_prompt_attention(q, k, v, ldq, ldk, ldv, cu_q, cu_k, S, Tq, Tk, H_q, H_kv, d, scale, out, lse_opt, ws,
                                      static_cast<cudaStream_t>(stream)))
     return MISA_ERR_UNSUPPORTED;
   return launch_status();

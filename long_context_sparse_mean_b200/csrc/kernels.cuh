@@ -229,7 +229,8 @@ void launch_evict_select(const float* acc, int64_t ld, const int32_t* n, int T, 
 // when the sizes or the missing tensor-map encoder rule it out.
 bool launch_prompt_attention(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
                              const int32_t* cu_q, const int32_t* cu_k, int S, int Tq, int Tk, int Hq, int Hkv, int d,
-                             float scale, void* out, float* lse, cudaStream_t s);
+                             float scale, void* out, float* lse, void* ws, cudaStream_t s);
+size_t prompt_ws_bytes(int S, int Tq, int Tk, int Hq, int d);  // 0: a call of few short items, no workspace
 
 int read_and_clear_prompt_status();  // as read_and_clear_tc_status
 int read_and_clear_compact_status();

@@ -29,7 +29,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
-#include <cstring>
+#include <algorithm>
 
 #include "kernels.cuh"
 #include "tc.cuh"
@@ -62,26 +62,17 @@ struct Lay {
   static constexpr int kOffQ = 0;
   static constexpr int kOffRing = 2 * kTileBytes;
   static constexpr int kOffBar = kOffRing + kBufs * kTileBytes;
-  static constexpr int kNumBars = 2 + 3 * kBufs + 8 + 1;
+  static constexpr int kNumBars = 3 * kBufs + 2 * 7 + 1;
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSmem = kOffMisc + 256 + 1024;      // + alignment slack
 };
 
-struct PromptArgs {
-  const __nv_bfloat16* v;
-  int64_t ldv;
-  const int32_t* cu_q;
-  const int32_t* cu_k;
-  int S, Tq, Tk, Hq, G;
-  float c;                // scale times log2(e)
-  __nv_bfloat16* out;
-  float* lse;
-};
-
-// What a CTA works on: rows [row, row + rows) of the queries, `keys` keys from key0 on; query i of the
-// pair sees keys j <= i + off.
-struct Item {
-  int row, rows, key0, keys, off, head;
+// Two consecutive tiles of queries of one sequence: rows [row, row + rows), which see keys of
+// [key0, key0 + keys); query i of them sees keys j <= i + off.  count: blocks of keys they read, at least 1
+// (an item that reads none still writes its outputs).
+struct __align__(16) Pair {
+  int row, rows, key0, keys;
+  int off, count, pad0, pad1;
   // blocks that tile t (0, 1) reads
   __device__ __forceinline__ int blocks(int t) const {
     if (t * kRows >= rows) return 0;
@@ -93,6 +84,58 @@ struct Item {
     const int end = (j + 1) * kRows;
     return end > keys || end - 1 > t * kRows + off;
   }
+};
+
+__device__ __forceinline__ Pair make_pair_of(int q0, int m, int k0, int l, int tile) {
+  Pair p;
+  p.row = q0 + tile * kPair;
+  p.rows = min(kPair, m - tile * kPair);
+  p.key0 = k0;
+  p.keys = l;
+  p.off = l - m + tile * kPair;
+  p.count = max(1, max(p.blocks(0), p.blocks(1)));
+  p.pad0 = p.pad1 = 0;
+  return p;
+}
+
+// A place between blocks: block j of the item (pair, head).
+struct __align__(16) Place {
+  int pair, head, j, pad;
+};
+
+// Where an item is cut by the boundary in front of a CTA: the CTAs first .. last hold its pieces; pair < 0
+// where nothing is cut, or the item's first cut lies further in front.
+struct __align__(16) Cut {
+  int pair, head, first, last;
+};
+
+// What a call of many or long items works from (prompt_plan_kernel): the pairs, and the sequence of items
+// (pair by pair, the heads of a pair one after another) cut into pieces of equal cost, CTA c's from
+// bounds[c] to bounds[c + 1].
+struct Plan {
+  Pair* pairs;     // null: CTA x takes item x, and no item is cut
+  Place* bounds;   // [kCtas + 1]
+  Cut* cuts;       // [kCtas]
+  uint64_t* cost;  // [pairs] running costs of one head's items
+  int most;        // room in `pairs`: what cu_q can hold where it does not decrease
+  float* part;     // [2 kCtas][D][kPair] sums of a CTA's first (cut in front) and last (cut behind) item
+  float* part_ml;  // [2 kCtas][2][kPair] their maxima and sums of weights
+};
+
+// An item costs its blocks and what its start and end take, in blocks.
+constexpr int kItemCost = 2;
+constexpr int kCtas = 148;
+
+struct PromptArgs {
+  const __nv_bfloat16* v;
+  int64_t ldv;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int S, Tq, Tk, Hq, G;
+  float c;                // scale times log2(e)
+  __nv_bfloat16* out;
+  float* lse;
+  Plan plan;
 };
 
 // Waits for the barrier phase with this parity; false once *abort is set or after the time limit.  The
@@ -175,60 +218,221 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       : "memory");
 }
 
-// Warp-wide: lane l writes 32 consecutive columns of TMEM lane (taddr.lane + l).
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+// Warp-wide: lane l writes 8 consecutive columns of TMEM lane (taddr.lane + l).
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Warp-wide: lane l reads 8 consecutive columns of TMEM lane (taddr.lane + l); the values are there on return.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(taddr)
       : "memory");
 }
 
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// The item of CTA x: pairs of every sequence from its last to its first (the longest come first), the
-// heads of a pair next to each other.  False when there is none.  Every thread of the block calls it.
-__device__ __forceinline__ bool find_item(const PromptArgs& a, int x, Item& it, uint32_t* warp_tot, int* found) {
-  const int pair = x / a.Hq;
-  it.head = x - pair * a.Hq;
+// Keys and queries of sequence b, clamped to the tensors: q0, m, k0, l.
+__device__ __forceinline__ int4 sequence(const PromptArgs& a, int b) {
+  const int q0 = max(0, __ldg(a.cu_q + b)), q1 = min(a.Tq, __ldg(a.cu_q + b + 1));
+  const int k0 = max(0, __ldg(a.cu_k + b)), k1 = min(a.Tk, __ldg(a.cu_k + b + 1));
+  return make_int4(q0, max(0, q1 - q0), k0, max(0, k1 - k0));
+}
+
+// Without a plan: the pair of CTA x / Hq, pairs of every sequence from its last to its first.  False when
+// there is none.  Every thread of the block calls it.
+__device__ __forceinline__ bool find_pair(const PromptArgs& a, int pair, Pair& p, uint32_t* warp_tot, Pair* found, int* hit) {
   int base = 0;
-  if (threadIdx.x == 0) found[0] = -1;
+  if (threadIdx.x == 0) *hit = 0;
   for (int b0 = 0; b0 < a.S; b0 += kThreads) {
     const int b = b0 + (int)threadIdx.x;
-    int q0 = 0, m = 0;
-    if (b < a.S) {
-      q0 = max(0, __ldg(a.cu_q + b));
-      m = max(0, min(a.Tq, __ldg(a.cu_q + b + 1)) - q0);
-    }
-    const int tiles = (m + kPair - 1) / kPair;
+    const int4 q = b < a.S ? sequence(a, b) : make_int4(0, 0, 0, 0);
+    const int tiles = (q.y + kPair - 1) / kPair;
     uint32_t total;
     const int before = base + (int)block_exclusive_scan((uint32_t)tiles, warp_tot, &total);
     if (pair >= before && pair < before + tiles) {
-      const int t = tiles - 1 - (pair - before);
-      const int k0 = max(0, __ldg(a.cu_k + b)), k1 = min(a.Tk, __ldg(a.cu_k + b + 1));
-      const int l = max(0, k1 - k0);
-      found[0] = q0 + t * kPair;
-      found[1] = min(kPair, m - t * kPair);
-      found[2] = k0;
-      found[3] = l;
-      found[4] = l - m + t * kPair;
+      *found = make_pair_of(q.x, q.y, q.z, q.w, tiles - 1 - (pair - before));
+      *hit = 1;
     }
     __syncthreads();
-    if (found[0] >= 0) break;
+    if (*hit) break;
     base += (int)total;
     if (base > pair) break;
   }
-  if (a.S <= 0 || found[0] < 0) return false;
-  it.row = found[0];
-  it.rows = found[1];
-  it.key0 = found[2];
-  it.keys = found[3];
-  it.off = found[4];
+  if (a.S <= 0 || !*hit) return false;
+  p = *found;
   return true;
+}
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanShared = 2048;  // pairs whose running costs fit in shared memory
+
+// The plan of one call, by one CTA.
+__global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptArgs a) {
+  __shared__ int base[kPlanThreads];
+  __shared__ uint32_t warp_tot[32];
+  __shared__ uint64_t run[kPlanShared];
+  __shared__ Place bounds[kCtas + 1];
+  __shared__ uint64_t carry;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int n = 0;
+  for (int b0 = 0; b0 < a.S; b0 += kPlanThreads) {
+    const int b = b0 + (int)threadIdx.x;
+    const int4 mine = b < a.S ? sequence(a, b) : make_int4(0, 0, 0, 0);
+    uint32_t total;
+    base[threadIdx.x] = n + (int)block_exclusive_scan((uint32_t)((mine.y + kPair - 1) / kPair), warp_tot, &total);
+    __syncthreads();
+    for (int x = warp; x < min(kPlanThreads, a.S - b0); x += kPlanThreads / 32) {
+      const int4 q = sequence(a, b0 + x);
+      const int tiles = (q.y + kPair - 1) / kPair;
+      for (int t = lane; t < tiles && base[x] + t < a.plan.most; t += 32)
+        a.plan.pairs[base[x] + t] = make_pair_of(q.x, q.y, q.z, q.w, t);
+    }
+    n = min(a.plan.most, n + (int)total);
+    __syncthreads();
+  }
+  // running costs
+  if (threadIdx.x == 0) carry = 0;
+  __syncthreads();
+  for (int p0 = 0; p0 < n; p0 += kPlanThreads) {
+    const int p = p0 + (int)threadIdx.x;
+    uint32_t total;
+    const uint32_t before = block_exclusive_scan(p < n ? (uint32_t)(a.plan.pairs[p].count + kItemCost) : 0u, warp_tot, &total);
+    if (p < n) {
+      const uint64_t v = carry + before;
+      a.plan.cost[p] = v;
+      if (p < kPlanShared) run[p] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) carry += total;
+    __syncthreads();
+  }
+  const uint64_t W = carry * a.Hq, parts = W < kCtas ? W : kCtas, slack = W / (16 * kCtas);
+  auto cost = [&](int p) { return p < kPlanShared ? run[p] : a.plan.cost[p]; };
+  const int c = threadIdx.x;
+  if (c <= kCtas) {
+    Place at = {n, 0, 0, 0};
+    const uint64_t x = c >= (int)parts ? W : W * c / parts;
+    if (x < W) {
+      int lo = 0, hi = n - 1;  // the last pair that starts at or before x
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cost(mid) * a.Hq <= x) lo = mid;
+        else hi = mid - 1;
+      }
+      const int blocks = a.plan.pairs[lo].count;
+      const uint64_t each = (uint64_t)(blocks + kItemCost), in = x - cost(lo) * a.Hq;
+      at.pair = lo;
+      at.head = (int)(in / each);
+      const uint64_t u = in - at.head * each;
+      // an item is not cut for a sixteenth of a share, nor inside its fixed cost
+      if (u <= kItemCost || u <= slack) {
+        at.j = 0;
+      } else if (each - u <= slack) {
+        at.j = 0;
+        if (++at.head == a.Hq) {
+          at.head = 0;
+          ++at.pair;
+        }
+      } else {
+        at.j = (int)(u - kItemCost);
+      }
+    }
+    bounds[c] = at;
+    a.plan.bounds[c] = at;
+  }
+  __syncthreads();
+  if (c < kCtas) {
+    Cut cut = {-1, 0, 0, 0};
+    const Place x = bounds[c];
+    auto same = [&](const Place& y) { return y.pair == x.pair && y.head == x.head && y.j > 0; };
+    if (c > 0 && x.j > 0 && !same(bounds[c - 1])) {
+      int last = c;
+      while (last + 1 < kCtas && same(bounds[last + 1])) ++last;
+      cut = {x.pair, x.head, c - 1, last};
+    }
+    a.plan.cuts[c] = cut;
+  }
+}
+
+// The work of one CTA, segment by segment: blocks [j0, j1) of the item (p, head).
+struct Walk {
+  Pair p;
+  int head, j0, j1;
+  int pair, end_pair, end_head, end_j;
+  __device__ __forceinline__ void take() { j1 = pair == end_pair && head == end_head ? end_j : p.count; }
+  // no segment left
+  __device__ __forceinline__ bool over() const {
+    return pair > end_pair || (pair == end_pair && (head > end_head || (head == end_head && j0 >= end_j)));
+  }
+  __device__ __forceinline__ void one(const Pair& q, int h) {
+    p = q;
+    head = h;
+    j0 = 0;
+    j1 = p.count;
+    pair = 0;
+    end_pair = 0;
+    end_head = h;
+    end_j = j1;
+  }
+  __device__ __forceinline__ bool begin(const PromptArgs& a, int cta) {
+    const Place x = a.plan.bounds[cta], e = a.plan.bounds[cta + 1];
+    pair = x.pair;
+    head = x.head;
+    j0 = x.j;
+    end_pair = e.pair;
+    end_head = e.head;
+    end_j = e.j;
+    if (over()) return false;
+    p = a.plan.pairs[pair];
+    take();
+    return true;
+  }
+  __device__ __forceinline__ bool advance(const PromptArgs& a) {
+    j0 = 0;  // a segment that others follow ends its item
+    ++head;
+    const bool next = head == a.Hq;
+    if (next) {
+      head = 0;
+      ++pair;
+    }
+    if (over()) return false;
+    if (next) p = a.plan.pairs[pair];
+    take();
+    return true;
+  }
+  // blocks of tile t in this segment
+  __device__ __forceinline__ int from(int t) const { return min(j0, p.blocks(t)); }
+  __device__ __forceinline__ int to(int t) const { return min(j1, p.blocks(t)); }
+  __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == p.count; }
+  // whether block j has keys that some query of the pair does not see
+  __device__ __forceinline__ bool guarded(int j) const {
+    return (j < p.blocks(0) && p.masked(0, j)) || (j < p.blocks(1) && p.masked(1, j));
+  }
+};
+
+// Adds to row i of a pair the values that are not finite and that it sees in blocks [from, to): the guards
+// took them out of those that some query does not see whole.  v: the kv head's first value of the
+// sequence; out (bf16, D in a row) or part (fp32, kPair apart): what this thread has just written.
+template <int D>
+__device__ __noinline__ void add_strange(const __nv_bfloat16* v, int64_t ldv, Pair p, int from, int to, int i,
+                                         __nv_bfloat16* out, float* part) {
+  const int end = min(p.keys, i + p.off + 1);
+  for (int k = from * kRows; k < min(end, to * kRows); ++k) {
+    const int j = k / kRows;
+    if (!((j < p.blocks(0) && p.masked(0, j)) || (j < p.blocks(1) && p.masked(1, j)))) continue;
+    for (int e = 0; e < D; ++e) {
+      const float f = __bfloat162float(v[k * ldv + e]);
+      if (isfinite(f)) continue;
+      if (out) out[e] = __float2bfloat16_rn(__bfloat162float(out[e]) + f);
+      else part[e * kPair] += f;
+    }
+  }
 }
 
 template <int D>
@@ -242,32 +446,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kOffMisc);
   volatile uint32_t* tmem_slot = misc;
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
-  volatile int* odd = reinterpret_cast<volatile int*>(misc + 2);  // a value that is not finite was set to zero
-  int* found = reinterpret_cast<int*>(misc + 4);
-  uint32_t* warp_tot = misc + 16;
+  // segment (plus one) in which a value that is not finite was set to zero, by its number modulo 4: guards
+  // and softmax are never as far apart
+  volatile int* odd = reinterpret_cast<volatile int*>(misc + 4);
+  Pair* found = reinterpret_cast<Pair*>(misc + 8);
+  uint32_t* warp_tot = misc + 20;
+  int* hit = reinterpret_cast<int*>(misc + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  Item it;
-  if (!find_item(a, blockIdx.x, it, warp_tot, found)) return;
-  const int nA = it.blocks(0), nB = it.blocks(1), nblk = max(nA, nB);
+  Walk walk;
+  if (a.plan.pairs == nullptr) {
+    Pair p;
+    if (!find_pair(a, blockIdx.x / a.Hq, p, warp_tot, found, hit)) return;
+    walk.one(p, blockIdx.x % a.Hq);
+  } else {
+    pdl_wait();
+    if (!walk.begin(a, blockIdx.x)) return;
+  }
 
   const uint32_t bar0 = tc::smem_u32(sm + L::kOffBar);
-  auto qfull = [&](int t) { return bar0 + 8 * t; };
-  auto full = [&](int i) { return bar0 + 8 * (2 + i); };
-  auto empty = [&](int i) { return bar0 + 8 * (2 + NB + i); };
-  auto vok = [&](int i) { return bar0 + 8 * (2 + 2 * NB + i); };
-  auto sfull = [&](int t) { return bar0 + 8 * (2 + 3 * NB + t); };
-  auto pfull = [&](int t) { return bar0 + 8 * (4 + 3 * NB + t); };
-  auto odone = [&](int t) { return bar0 + 8 * (6 + 3 * NB + t); };
-  auto phalf = [&](int t) { return bar0 + 8 * (8 + 3 * NB + t); };
-  const uint32_t drain = bar0 + 8 * (10 + 3 * NB);
+  auto full = [&](int i) { return bar0 + 8 * i; };
+  auto empty = [&](int i) { return bar0 + 8 * (NB + i); };
+  auto vok = [&](int i) { return bar0 + 8 * (2 * NB + i); };
+  auto qfull = [&](int t) { return bar0 + 8 * (3 * NB + t); };
+  auto qempty = [&](int t) { return bar0 + 8 * (3 * NB + 2 + t); };
+  auto sfull = [&](int t) { return bar0 + 8 * (3 * NB + 4 + t); };
+  auto phalf = [&](int t) { return bar0 + 8 * (3 * NB + 6 + t); };
+  auto pfull = [&](int t) { return bar0 + 8 * (3 * NB + 8 + t); };
+  auto odone = [&](int t) { return bar0 + 8 * (3 * NB + 10 + t); };
+  auto oread = [&](int t) { return bar0 + 8 * (3 * NB + 12 + t); };
+  const uint32_t drain = bar0 + 8 * (3 * NB + 14);
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(qfull(t), 1);
+      tc::mbar_init(qempty(t), 1);
       tc::mbar_init(sfull(t), 1);
-      tc::mbar_init(pfull(t), 4);
       tc::mbar_init(phalf(t), 4);
+      tc::mbar_init(pfull(t), 4);
       tc::mbar_init(odone(t), 1);
+      tc::mbar_init(oread(t), 4);
     }
     for (int i = 0; i < NB; ++i) {
       tc::mbar_init(full(i), 1);
@@ -276,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::mbar_init(drain, 1);
     *abort = 0;
-    *odd = 0;
+    for (int x = 0; x < 4; ++x) odd[x] = 0;
     tc::mbar_init_fence();
   }
   if (warp == kMmaWarp) {
@@ -288,21 +505,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t qbase = tc::smem_u32(sm + L::kOffQ), ring = tc::smem_u32(sm + L::kOffRing);
-  // block j's K is ring use 2 j, its V use 2 j + 1
-  auto guarded = [&](int j) { return (j < nA && it.masked(0, j)) || (j < nB && it.masked(1, j)); };
+  // every segment's blocks j0 .. j1 - 1 take turns in the ring, K before V
 
   if (warp < 8) {
     // ---------------- softmax ----------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int t = warp >> 2, n = t ? nB : nA;
+    const int t = warp >> 2;
     const int i = t * kRows + (warp & 3) * 32 + lane;  // query of the pair
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * kRows, to = tmem + lanes + 2 * kRows + t * kRows;
     const float c = a.c;
-    float m = -INFINITY, l = 0.f;  // maximum of the raw scores, sum of the weights
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!wait_for(sfull(t), j & 1, abort)) {
+    uint32_t done = 0;  // blocks of this tile so far
+    for (int seg = 0;; ++seg) {
+    const int from = walk.from(t), to_ = walk.to(t);
+    float m = -INFINITY, l = 0.f;  // maximum of the raw scores, sum of the weights
+    for (int j = from; j < to_; ++j, ++done) {
+      if (!wait_for(sfull(t), done & 1, abort)) {
         ok = false;
         break;
       }
@@ -312,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < 4; ++x) tc::tmem_ld32(ts + 32 * x, s[x]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) tc::tmem_ld_wait(s[x]);
-      if (it.masked(t, j)) {
-        const int seen = min(it.keys, i + it.off + 1) - j * kRows;  // keys of this block that row i sees
+      if (walk.p.masked(t, j)) {
+        const int seen = min(walk.p.keys, i + walk.p.off + 1) - j * kRows;  // keys of this block that row i sees
 #pragma unroll
         for (int x = 0; x < 4; ++x) hide(s[x], seen - 32 * x);
       }
@@ -352,9 +571,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
       const bool raise = mx * c > m * c + kSlack;  // also the first score that is seen
       if (__any_sync(0xffffffffu, raise)) {
-        if (j > 0) {
-          // O holds blocks 0 .. j - 1 once their product is through
-          if (!wait_for(odone(t), (j - 1) & 1, abort)) {
+        if (j > from) {
+          // O holds the blocks before this one once their product is through
+          if (!wait_for(odone(t), (done - 1) & 1, abort)) {
             ok = false;
             break;
           }
@@ -362,13 +581,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = raise && m != -INFINITY ? ex2((m - mx) * c) : 1.f;
           l *= f;
 #pragma unroll 1
-          for (int x = 0; x < D / 32; ++x) {
-            uint32_t o[32];
-            tc::tmem_ld32(to + 32 * x, o);
-            tc::tmem_ld_wait(o);
+          for (int x = 0; x < D; x += 8) {
+            uint32_t o[8];
+            tmem_ld8(to + x, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(to + 32 * x, o);
+            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st8(to + x, o);
           }
         }
         if (raise) m = mx;
@@ -402,102 +620,103 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) tc::mbar_arrive_relaxed(pfull(t));  // what it hands on lies in tensor memory
     }
-    if (ok && n > 0 && !wait_for(odone(t), (n - 1) & 1, abort)) ok = false;
+    if (ok && to_ > from && !wait_for(odone(t), (done - 1) & 1, abort)) ok = false;
+    if (!ok) {
+      give_up(abort);
+      break;
+    }
     tc::tc_fence_after();
-    if (!ok) give_up(abort);
-    if (ok && t * kRows < it.rows) {
-      const int64_t row = (int64_t)it.row + i;
+    const Pair& p = walk.p;
+    const bool whole = walk.whole();
+    if (t * kRows + (warp & 3) * 32 < p.rows || to_ > from) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      // this warp's 32 rows go through its share of the Q tile, which the products have read
-      uint8_t* stage = sm + L::kOffQ + t * L::kTileBytes + (warp & 3) * 32 * D * 2;
-      constexpr int CH = D / 8;  // 16-byte pieces of a row
+      const int slot = 2 * blockIdx.x + (walk.j0 == 0 ? 1 : 0);
+      __nv_bfloat16* out = a.out + ((int64_t)(p.row + i) * a.Hq + walk.head) * D;
+      float* part = a.plan.part + (int64_t)slot * D * kPair + i;
+      // eight outputs at a time, in a loop of few instructions: once an item, this code is not in the
+      // instruction cache when it runs
 #pragma unroll 1
-      for (int x = 0; x < D / 32; ++x) {
-        uint32_t o[32];
-        if (n > 0) {
-          tc::tmem_ld32(to + 32 * x, o);
-          tc::tmem_ld_wait(o);
+      for (int x = 0; x < D; x += 8) {
+        uint32_t o[8];
+        if (to_ > from) {
+          tmem_ld8(to + x, o);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
+          for (int e = 0; e < 8; ++e) o[e] = 0u;
         }
-        if (*odd) {  // values that are not finite and that this row sees, in the blocks they were taken out of
-          const int end = min(it.keys, i + it.off + 1);
-          for (int j = 0; j < n; ++j) {
-            if (!guarded(j)) continue;
-            for (int k = j * kRows; k < min(end, (j + 1) * kRows); ++k) {
-              const __nv_bfloat16* vr = a.v + (int64_t)(it.key0 + k) * a.ldv + (it.head / a.G) * D + 32 * x;
-              for (int e = 0; e < 32; ++e) {
-                const float f = __bfloat162float(vr[e]);
+        if (!whole) {
 #pragma unroll
-                for (int y = 0; y < 32; ++y)
-                  if (y == e && !isfinite(f)) o[y] = __float_as_uint(__uint_as_float(o[y]) + f);
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
+          for (int e = 0; e < 8; ++e) part[(x + e) * kPair] = __uint_as_float(o[e]);
+        } else {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * y + 2 * e]) * inv,
-                                                           __uint_as_float(o[8 * y + 2 * e + 1]) * inv);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
             w[e] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          const int piece = 4 * x + y;
-          *reinterpret_cast<uint4*>(stage + lane * (D * 2) + ((piece ^ (lane & (CH - 1))) * 16)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          if (i < p.rows) *reinterpret_cast<uint4*>(out + x) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      __syncwarp();
-      constexpr int RPI = 32 / CH;  // rows a store instruction covers
-      const int first = t * kRows + (warp & 3) * 32;
-#pragma unroll 4
-      for (int y = 0; y < 32; y += RPI) {
-        const int rr = y + lane / CH, piece = lane % CH;
-        if (first + rr < it.rows)
-          *reinterpret_cast<uint4*>(a.out + ((int64_t)(it.row + first + rr) * a.Hq + it.head) * D + piece * 8) =
-              *reinterpret_cast<const uint4*>(stage + rr * (D * 2) + ((piece ^ (rr & (CH - 1))) * 16));
+      if (to_ > from) {  // the next segment may overwrite O
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_relaxed(oread(t));
       }
-      if (a.lse && i < it.rows)
-        a.lse[row * a.Hq + it.head] = l == 0.f ? -INFINITY : m * c * 0.693147180559945309f + logf(l);
+      if (!whole) {
+        a.plan.part_ml[(slot * 2) * kPair + i] = m;
+        a.plan.part_ml[(slot * 2 + 1) * kPair + i] = l;
+      } else if (a.lse && i < p.rows) {
+        a.lse[((int64_t)p.row + i) * a.Hq + walk.head] = l == 0.f ? -INFINITY : m * c * 0.693147180559945309f + logf(l);
+      }
+      if (odd[seg & 3] == seg + 1 && i < p.rows)
+        add_strange<D>(a.v + (int64_t)p.key0 * a.ldv + (walk.head / a.G) * D, a.ldv, p, from, to_, i,
+                       whole ? out : nullptr, part);
+    }
+    if (!walk.advance(a)) break;
     }
   } else {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kLoadWarp) {
     // ---------------- TMA producer ----------------
     if (elect_one()) {
-      const int hk = it.head / a.G;
       bool ok = true;
-      uint32_t u = 0;
-      auto q_tile = [&](int t) {
-        tc::mbar_arrive_expect_tx(qfull(t), L::kTileBytes);
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-          tc::tma_load_2d(qbase + t * L::kTileBytes + x * L::kHalfBytes, &qmap, it.head * D + x * 64,
-                          it.row + t * kRows, qfull(t));
+      uint32_t u = 0, q[2] = {0, 0};  // ring buffers and Q tiles filled so far
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok && !wait_for(bar, parity, abort)) ok = false;
+        return ok;
       };
-      if (nA > 0) q_tile(0);
-      for (int j = 0; ok && j < nblk; ++j) {
-        for (int side = 0; side < 2; ++side, ++u) {
-          const int b = u % NB;
-          if (u >= NB && !wait_for(empty(b), ((u / NB) - 1) & 1, abort)) {
-            ok = false;
-            break;
-          }
-          tc::mbar_arrive_expect_tx(full(b), L::kTileBytes);
+      do {
+        const Pair& p = walk.p;
+        const int hk = walk.head / a.G;
+        const bool has[2] = {walk.to(0) > walk.from(0), walk.to(1) > walk.from(1)};
+        auto q_tile = [&](int t) {
+          if (q[t] > 0 && !wait(qempty(t), (q[t] - 1) & 1)) return;
+          ++q[t];
+          tc::mbar_arrive_expect_tx(qfull(t), L::kTileBytes);
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
-            tc::tma_load_2d(ring + b * L::kTileBytes + x * L::kHalfBytes, side ? &vmap : &kmap, hk * D + x * 64,
-                            it.key0 + j * kRows, full(b));
-          if (j == 0 && side == 0 && nB > 0) q_tile(1);
+            tc::tma_load_2d(qbase + t * L::kTileBytes + x * L::kHalfBytes, &qmap, walk.head * D + x * 64,
+                            p.row + t * kRows, qfull(t));
+        };
+        const int j1 = max(walk.to(0), walk.to(1));
+        if (has[0]) q_tile(0);
+        for (int j = walk.j0; ok && j < j1; ++j) {
+          for (int side = 0; ok && side < 2; ++side, ++u) {
+            const int b = u % NB;
+            if (u >= NB && !wait(empty(b), ((u / NB) - 1) & 1)) break;
+            tc::mbar_arrive_expect_tx(full(b), L::kTileBytes);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              tc::tma_load_2d(ring + b * L::kTileBytes + x * L::kHalfBytes, side ? &vmap : &kmap, hk * D + x * 64,
+                              p.key0 + j * kRows, full(b));
+            if (j == walk.j0 && side == 0 && has[1]) q_tile(1);
+          }
         }
-      }
+      } while (ok && walk.advance(a));
       if (!ok) give_up(abort);
       // every issued copy lands before the CTA exits
-      if (nA > 0) wait_for(qfull(0), 0, nullptr);
-      if (nB > 0) wait_for(qfull(1), 0, nullptr);
+      for (int t = 0; t < 2; ++t)
+        if (q[t] > 0) wait_for(qfull(t), (q[t] - 1) & 1, nullptr);
       for (uint32_t g = u > NB ? u - NB : 0; g < u; ++g) wait_for(full(g % NB), (g / NB) & 1, nullptr);
     }
   } else if (warp == kMmaWarp) {
@@ -510,43 +729,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && !wait_for(bar, parity, abort)) ok = false;
         return ok;
       };
-      auto scores = [&](int t, int j) {  // S_t = Q_t K_j^T
-        const uint32_t u = 2 * j, b = u % NB;
-        if (j == 0 && !wait(qfull(t), 0)) return;
+      // One segment's blocks of either tile, [f0, t0) and [f1, t1), and the ring turn of its block j0
+      struct Seg {
+        int f0, t0, f1, t1, j0, j1;
+        uint32_t turn;
+        __device__ __forceinline__ int from(int t) const { return t ? f1 : f0; }
+        __device__ __forceinline__ int to(int t) const { return t ? t1 : t0; }
+        // the last tile that reads block j
+        __device__ __forceinline__ bool last(int t, int j) const { return t == 1 || j < f1 || j >= t1; }
+      };
+      auto segment = [&](uint32_t turn) {
+        Seg g;
+        g.f0 = walk.from(0);
+        g.t0 = walk.to(0);
+        g.f1 = walk.from(1);
+        g.t1 = walk.to(1);
+        g.j0 = walk.j0;
+        g.j1 = max(g.t0, g.t1);
+        g.turn = turn;
+        return g;
+      };
+      uint32_t qn0 = 0, qn1 = 0, on0 = 0, on1 = 0, dn0 = 0, dn1 = 0;  // Q tiles, outputs and blocks begun, by tile
+      auto scores = [&](const Seg& g, const int t, int j) {  // S_t = Q_t K_j^T
+        const uint32_t u = g.turn + 2 * (j - g.j0), b = u % NB;
+        if (j == g.from(t)) {
+          uint32_t& qn = t ? qn1 : qn0;
+          if (!wait(qfull(t), qn & 1)) return;
+          ++qn;
+        }
         if (!wait(full(b), (u / NB) & 1)) return;
+        const uint64_t qd = tc::sw128_kmajor_desc(qbase + t * L::kTileBytes), kd = tc::sw128_kmajor_desc(ring + b * L::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = (kk / 4) * L::kHalfBytes + (kk % 4) * 32;
-          tc::mma_bf16(tmem + t * kRows, tc::sw128_kmajor_desc(qbase + t * L::kTileBytes + at),
-                       tc::sw128_kmajor_desc(ring + b * L::kTileBytes + at), idesc_s, kk != 0);
+          const uint32_t at = ((kk / 4) * L::kHalfBytes + (kk % 4) * 32) >> 4;
+          tc::mma_bf16(tmem + t * kRows, qd + at, kd + at, idesc_s, kk != 0);
         }
         tc::mma_commit(sfull(t));
-        if (t == 1 || j >= nB) tc::mma_commit(empty(b));
+        if (j + 1 == g.to(t)) tc::mma_commit(qempty(t));
+        if (g.last(t, j)) tc::mma_commit(empty(b));
       };
-      auto values = [&](int t, int j) {  // O_t += P_t V_j
-        const uint32_t u = 2 * j + 1, b = u % NB;
+      auto values = [&](const Seg& g, const int t, int j) {  // O_t += P_t V_j
+        const uint32_t u = g.turn + 2 * (j - g.j0) + 1, b = u % NB;
+        uint32_t& dn = t ? dn1 : dn0;
         if (!wait(vok(b), (u / NB) & 1)) return;
+        if (j == g.from(t)) {
+          uint32_t& on = t ? on1 : on0;
+          if (on > 0 && !wait(oread(t), (on - 1) & 1)) return;
+          ++on;
+        }
+        const uint64_t vd = sw128_mnmajor_desc(ring + b * L::kTileBytes, L::kHalfBytes);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          if (!wait(half ? pfull(t) : phalf(t), j & 1)) return;
+          if (!wait(half ? pfull(t) : phalf(t), dn & 1)) return;
           tc::tc_fence_after();  // after the weights' stores to tensor memory, by other threads
 #pragma unroll
           for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            mma_bf16_ts(tmem + 2 * kRows + t * kRows, tmem + t * kRows + kk * 8,
-                        sw128_mnmajor_desc(ring + b * L::kTileBytes + kk * 2048, L::kHalfBytes), idesc_o,
-                        (j | kk) != 0);
+            mma_bf16_ts(tmem + 2 * kRows + t * kRows, tmem + t * kRows + kk * 8, vd + kk * (2048 >> 4), idesc_o,
+                        (j > g.from(t)) || kk != 0);
         }
         tc::mma_commit(odone(t));
-        if (t == 1 || j >= nB) tc::mma_commit(empty(b));
+        if (g.last(t, j)) tc::mma_commit(empty(b));
+        ++dn;
       };
-      if (nA > 0) scores(0, 0);
-      if (nB > 0 && ok) scores(1, 0);
-      for (int j = 0; ok && j < nblk; ++j) {
-        for (int t = 0; ok && t < 2; ++t) {
-          const int n = t ? nB : nA;
-          if (j < n) values(t, j);
-          if (ok && j + 1 < n) scores(t, j + 1);
+      Seg g = segment(0);
+      if (g.t0 > g.f0) scores(g, 0, g.f0);
+      if (ok && g.t1 > g.f1) scores(g, 1, g.f1);
+      while (ok) {
+        const bool more = walk.advance(a);
+        Seg next = g;
+        if (more) next = segment(g.turn + 2 * (uint32_t)max(0, g.j1 - g.j0));
+        // a tile's first scores of the next segment follow its last block of this one, unless the other tile
+        // has more than one block to go: the ring could not hold what lies between
+        bool begun0 = false, begun1 = false;
+        for (int j = g.j0; ok && j < g.j1; ++j) {
+          const bool ahead = more && j + 2 >= g.j1;
+          if (j >= g.f0 && j < g.t0) {
+            values(g, 0, j);
+            if (ok && j + 1 < g.t0) {
+              scores(g, 0, j + 1);
+            } else if (ok && ahead && next.t0 > next.f0) {
+              scores(next, 0, next.f0);
+              begun0 = true;
+            }
+          }
+          if (ok && j >= g.f1 && j < g.t1) {
+            values(g, 1, j);
+            if (ok && j + 1 < g.t1) {
+              scores(g, 1, j + 1);
+            } else if (ok && ahead && j + 1 == g.j1 && next.t1 > next.f1 && (begun0 || next.t0 <= next.f0)) {
+              // (behind the first tile's: the second one's use of a block is taken to be the last)
+              scores(next, 1, next.f1);
+              begun1 = true;
+            }
+          }
         }
+        if (!ok || !more) break;
+        g = next;
+        if (!begun0 && g.t0 > g.f0) scores(g, 0, g.f0);
+        if (ok && !begun1 && g.t1 > g.f1) scores(g, 1, g.f1);
       }
       if (!ok) give_up(abort);
       // every issued MMA completes before tensor memory is freed
@@ -556,46 +836,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- guards ----------------
     bool ok = true;
-    for (int j = 0; ok && j < nblk; ++j) {
-      const uint32_t u = 2 * j + 1, b = u % NB;
+    uint32_t u = 1;  // ring turn of the next V
+    for (int seg = 0;; ++seg) {
+    for (int j = walk.j0; ok && j < max(walk.to(0), walk.to(1)); ++j, u += 2) {
+      const uint32_t b = u % NB;
       if (!wait_for(full(b), (u / NB) & 1, abort)) {
         ok = false;
         break;
       }
-      if (!guarded(j)) {  // passed on all the same: a guard that fell behind by a turn of the ring would miss its phase
+      if (!walk.guarded(j)) {  // passed on all the same: a guard that fell behind by a turn of the ring would miss its phase
         if (lane == 0) tc::mbar_arrive(vok(b));
         continue;
       }
-      const int there = it.keys - j * kRows;  // rows from here on belong to no key of the sequence
+      const int there = walk.p.keys - j * kRows;  // rows from here on belong to no key of the sequence
       const int first = (warp - kGuardWarp) * (kRows / 2);
       uint8_t* v = sm + L::kOffRing + b * L::kTileBytes;
+      // a 16-bit number whose exponent is all ones carries into its top bit
+      auto hit = [](uint32_t z) { return ((z & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+      auto clean = [&](uint32_t z) { return z & ~((hit(z) >> 15) * 0xffffu); };
+      constexpr int kPieces = (kRows / 2) * (D / 8);  // of 16 bytes, 8 a row and box of 64 dims
+      auto piece = [&](int x) {
+        const int half = x / (kRows / 2 * 8), y = x % (kRows / 2 * 8);
+        return reinterpret_cast<uint4*>(v + half * L::kHalfBytes + (first + y / 8) * 128 + (y % 8) * 16);
+      };
       bool changed = false, bad = false;
-#pragma unroll 4
-      for (int x = lane; x < (kRows / 2) * (D / 8); x += 32) {
-        const int half = x / (kRows / 2 * 8), y = x % (kRows / 2 * 8);  // 8 pieces of 16 bytes a row and half
-        const int r = first + y / 8;
-        uint4* p = reinterpret_cast<uint4*>(v + half * L::kHalfBytes + r * 128 + (y % 8) * 16);
-        if (r >= there) {
-          *p = make_uint4(0u, 0u, 0u, 0u);
-          changed = true;
-          continue;
-        }
-        const uint4 w = *p;
-        // a half whose exponent is all ones carries into its top bit
-        auto hit = [](uint32_t z) { return ((z & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-        if (hit(w.x) | hit(w.y) | hit(w.z) | hit(w.w)) {
-          auto clean = [&](uint32_t z) {
-            const uint32_t h = hit(z);
-            return z & ~((h >> 15) * 0xffffu);
-          };
-          *p = make_uint4(clean(w.x), clean(w.y), clean(w.z), clean(w.w));
+      if (first + kRows / 2 > there) {
+        for (int x = lane; x < kPieces; x += 32)
+          if (first + x % (kRows / 2 * 8) / 8 >= there) *piece(x) = make_uint4(0u, 0u, 0u, 0u);
+        changed = true;
+      }
+#pragma unroll 1
+      for (int x0 = lane; x0 < kPieces; x0 += 32 * 8) {
+        uint4 w[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) w[y] = *piece(x0 + 32 * y);
+        uint32_t any = 0;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) any |= hit(w[y].x) | hit(w[y].y) | hit(w[y].z) | hit(w[y].w);
+        if (any) {
+#pragma unroll 1
+          for (int y = 0; y < 8; ++y) {
+            uint4* p = piece(x0 + 32 * y);
+            const uint4 z = *p;
+            *p = make_uint4(clean(z.x), clean(z.y), clean(z.z), clean(z.w));
+          }
           changed = bad = true;
         }
       }
-      if (bad) *odd = 1;
+      if (bad) odd[seg & 3] = seg + 1;
       if (changed) tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(vok(b));
+    }
+    if (!ok || !walk.advance(a)) break;
     }
     if (!ok) give_up(abort);
   }
@@ -607,6 +900,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Joins the pieces of the items that a boundary between CTAs cuts: CTA (c, y) takes 16 output columns of
+// the item whose first cut lies in front of CTA c + 1, one thread a row.
+template <int D>
+__global__ void __launch_bounds__(kPair) prompt_join_kernel(const PromptArgs a) {
+  pdl_wait();
+  const Cut cut = a.plan.cuts[blockIdx.x + 1];
+  if (cut.pair < 0) return;
+  const Pair p = a.plan.pairs[cut.pair];
+  const int i = threadIdx.x, d0 = blockIdx.y * 16;
+  if (i >= p.rows) return;
+  // the first piece is its CTA's last, the others their CTAs' first
+  auto slot = [&](int c) { return 2 * c + (c == cut.first ? 1 : 0); };
+  float top = -INFINITY;
+  for (int c = cut.first; c <= cut.last; ++c) top = fmaxf(top, a.plan.part_ml[(slot(c) * 2) * kPair + i]);
+  float sum = 0.f, o[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
+  for (int c = cut.first; c <= cut.last; ++c) {
+    const int s = slot(c);
+    const float l = a.plan.part_ml[(s * 2 + 1) * kPair + i];
+    if (l == 0.f) continue;  // saw nothing
+    const float f = ex2((a.plan.part_ml[(s * 2) * kPair + i] - top) * a.c);
+    sum += f * l;
+    const float* src = a.plan.part + ((int64_t)s * D + d0) * kPair + i;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] += f * src[e * kPair];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(a.out + ((int64_t)(p.row + i) * a.Hq + cut.head) * D + d0);
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  if (a.lse && blockIdx.y == 0)
+    a.lse[((int64_t)p.row + i) * a.Hq + cut.head] =
+        sum == 0.f ? -INFINITY : top * a.c * 0.693147180559945309f + logf(sum);
 }
 
 // Map over packed rows [rows][cols] of bf16 at a stride of ld elements, boxes of 64 columns x 128 rows in
@@ -623,22 +958,42 @@ bool row_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int64_t most_pairs(int S, int Tq) { return (int64_t)Tq / kPair + std::min(S, Tq); }
+
+// Whether a call goes without a plan, one item a CTA: few enough items for one CTA an SM, none of them long
+// (32 blocks of keys at most), so that cutting them up would not pay for the two launches it adds.
+bool plain_call(int S, int Tq, int Tk, int Hq) { return most_pairs(S, Tq) * Hq <= kCtas && Tk <= 32 * kRows; }
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
 template <int D>
 bool launch_d(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm, const PromptArgs& a,
               cudaStream_t s) {
   static_assert(Lay<D>::kSmem <= 232448, "shared memory of the prompt kernel exceeds 227 KB");
-  const int64_t grid = ((int64_t)a.Tq / kPair + std::min<int64_t>(a.S, a.Tq)) * a.Hq;
-  if (grid > INT32_MAX) return false;
-  cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem);
-  prompt_kernel<D><<<(unsigned)grid, kThreads, Lay<D>::kSmem, s>>>(qm, km, vm, a);
+  if (cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem) != cudaSuccess)
+    return false;
+  if (a.plan.pairs == nullptr) {
+    prompt_kernel<D><<<(unsigned)(most_pairs(a.S, a.Tq) * a.Hq), kThreads, Lay<D>::kSmem, s>>>(qm, km, vm, a);
+    return true;
+  }
+  prompt_plan_kernel<<<1, kPlanThreads, 0, s>>>(a);
+  launch_pdl(prompt_kernel<D>, dim3(kCtas), dim3(kThreads), Lay<D>::kSmem, s, qm, km, vm, a);
+  launch_pdl(prompt_join_kernel<D>, dim3(kCtas - 1, D / 16), dim3(kPair), 0, s, a);
   return true;
 }
 
 }  // namespace
 
+size_t prompt_ws_bytes(int S, int Tq, int Tk, int Hq, int d) {
+  if (S <= 0 || Tq <= 0 || plain_call(S, Tq, Tk, Hq)) return 0;
+  return up256(sizeof(Pair) * most_pairs(S, Tq)) + up256(sizeof(Place) * (kCtas + 1)) + up256(sizeof(Cut) * kCtas) +
+         up256(sizeof(uint64_t) * most_pairs(S, Tq)) +
+         up256(sizeof(float) * 2 * kCtas * (size_t)kPair * d) + up256(sizeof(float) * 4 * kCtas * kPair);
+}
+
 bool launch_prompt_attention(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
                              const int32_t* cu_q, const int32_t* cu_k, int S, int Tq, int Tk, int Hq, int Hkv, int d,
-                             float scale, void* out, float* lse, cudaStream_t s) {
+                             float scale, void* out, float* lse, void* ws, cudaStream_t s) {
   if (S <= 0 || Tq <= 0) return true;
   CUtensorMap qm, km, vm;
   if (!row_map(&qm, q, (int64_t)Hq * d, Tq, ldq)) return false;
@@ -658,6 +1013,22 @@ bool launch_prompt_attention(const void* q, const void* k, const void* v, int64_
   a.c = scale * 1.44269504088896341f;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
+  a.plan = {};
+  if (!plain_call(S, Tq, Tk, Hq)) {
+    char* p = static_cast<char*>(ws);
+    a.plan.pairs = reinterpret_cast<Pair*>(p);
+    p += up256(sizeof(Pair) * most_pairs(S, Tq));
+    a.plan.bounds = reinterpret_cast<Place*>(p);
+    p += up256(sizeof(Place) * (kCtas + 1));
+    a.plan.cuts = reinterpret_cast<Cut*>(p);
+    p += up256(sizeof(Cut) * kCtas);
+    a.plan.cost = reinterpret_cast<uint64_t*>(p);
+    p += up256(sizeof(uint64_t) * most_pairs(S, Tq));
+    a.plan.most = (int)most_pairs(S, Tq);
+    a.plan.part = reinterpret_cast<float*>(p);
+    p += up256(sizeof(float) * 2 * kCtas * (size_t)kPair * d);
+    a.plan.part_ml = reinterpret_cast<float*>(p);
+  }
   return d == 128 ? launch_d<128>(qm, km, vm, a, s) : launch_d<64>(qm, km, vm, a, s);
 }
 

@@ -44,7 +44,7 @@ COMPACT = dict(pool=FAKE, np=100, ps=64, table=FAKE, mp=10, idx=FAKE, T=4, keep=
 KEYS = dict(pool=FAKE, np=100, ps=64, table=FAKE, mp=10, idx=FAKE, T=4, keep=100, d=128, dt=BF16, ws=FAKE, wsb=1 << 30,
             s=None)
 PROMPT = dict(q=FAKE, k=FAKE, v=FAKE, ldq=4096, ldk=1024, ldv=1024, cuq=FAKE, cuk=FAKE, S=2, Tq=8, Tk=8, Hq=32, H=8,
-              d=128, dt=BF16, scale=0.1, out=FAKE, lse=None, s=None)
+              d=128, dt=BF16, scale=0.1, out=FAKE, lse=None, ws=FAKE, wsb=1 << 30, s=None)
 
 
 @pytest.mark.parametrize("name,base", [("misa_kv4_append", APPEND), ("misa_kv4_read", READ)])
@@ -102,6 +102,7 @@ def test_prompt_refusals(lib):
                      (dict(scale=-0.1), INVALID), (dict(scale=INF), INVALID), (dict(q=None), INVALID), (dict(k=BENT), INVALID),
                      (dict(ldq=4092), INVALID), (dict(ldk=1016), INVALID), (dict(ldv=1027), INVALID), (dict(out=None), INVALID),
                      (dict(out=BENT), INVALID), (dict(cuq=None), INVALID), (dict(cuk=None), INVALID),
+                     (dict(Tq=9000, ws=None), WORKSPACE), (dict(Tq=9000, ws=BENT), WORKSPACE), (dict(Tq=9000, wsb=1000), WORKSPACE),
                      (dict(Tq=0, q=None, out=None), OK), (dict(S=0, cuq=None), OK)]:
         assert call(lib.misa_prompt_attention, PROMPT, **kw) == want, kw
 

@@ -77,6 +77,27 @@ def test_longer_prompts(d):
     M.misa_device_check()
 
 
+@pytest.mark.parametrize("d,Hq,Hkv,lens,extra", [
+    (128, 4, 2, [130], [20000]),                     # two items a head, cut between all CTAs
+    (64, 2, 1, [1], [9000]),
+    (128, 1, 1, [300, 1, 257], [5000, 0, -200]),     # items of every length, some queries before the first key
+    (64, 24, 8, [400, 0, 90, 1, 700, 256, 33] * 3, [0] * 21),   # more items than CTAs
+    (128, 16, 2, [64] * 60 + [900], [0] * 60 + [3000]),
+])
+def test_items_cut_between_ctas(d, Hq, Hkv, lens, extra):
+    M = lib()
+    rng = np.random.default_rng(d + len(lens))
+    cu_q, cu_k = cum(lens), cum([a + b for a, b in zip(lens, extra)])
+    q = cuda(rng.standard_normal((cu_q[-1], Hq, d)).astype(np.float32) * 2, torch.bfloat16)
+    k, v = (cuda(rng.standard_normal((cu_k[-1], Hkv, d)).astype(np.float32), torch.bfloat16) for _ in range(2))
+    assert M.misa_workspace_bytes(M.OP_PROMPT_ATTENTION, int(cu_q[-1]), int(cu_k[-1]), Hq, len(lens), d) > 0
+    out, lse = M.misa_prompt_attention(q, k, v, cuda(cu_q), cuda(cu_k), want_lse=True)
+    check(M, q, k, v, cu_q, cu_k, out, lse, d ** -0.5, rows=12)
+    again, al = M.misa_prompt_attention(q, k, v, cuda(cu_q), cuda(cu_k), want_lse=True)
+    assert torch.equal(out, again) and torch.equal(lse, al)
+    M.misa_device_check()
+
+
 def test_sharp_and_flat_logits_and_growing_maxima():
     M = lib()
     rng = np.random.default_rng(5)
@@ -109,6 +130,17 @@ def test_views_of_a_fused_projection_and_rows_of_no_sequence():
         assert (x[:10] == 5).all() and (x[401:] == 5).all()
 
 
+def test_more_sequences_than_threads():
+    M = lib()
+    rng = np.random.default_rng(16)
+    lens = rng.integers(0, 5, 1100)
+    cu = cum(lens)
+    q = cuda(rng.standard_normal((cu[-1], 2, 64)).astype(np.float32), torch.bfloat16)
+    k, v = (cuda(rng.standard_normal((cu[-1], 1, 64)).astype(np.float32), torch.bfloat16) for _ in range(2))
+    out, lse = M.misa_prompt_attention(q, k, v, cuda(cu), want_lse=True)
+    check(M, q, k, v, cu, cu, out, lse, 0.125)
+
+
 @pytest.mark.parametrize("junk", [float("nan"), float("inf"), -float("inf")])
 def test_rows_of_other_sequences_do_not_reach_a_sequence(junk):
     """Keys and values next to a sequence that are not finite change nothing in it."""
@@ -133,9 +165,9 @@ def test_tokens_behind_a_query_do_not_reach_it(junk):
     """A key and value that are not finite change no earlier token's output."""
     M = lib()
     rng = np.random.default_rng(8)
-    for n, at in ((300, 150), (300, 290), (1000, 513)):
+    for n, at, Hq in ((300, 150, 4), (300, 290, 4), (1000, 513, 4), (1000, 513, 64), (5000, 4444, 4)):
         cu = cum([n])
-        q = cuda(rng.standard_normal((n, 4, 64)).astype(np.float32), torch.bfloat16)
+        q = cuda(rng.standard_normal((n, Hq, 64)).astype(np.float32), torch.bfloat16)
         k, v = (cuda(rng.standard_normal((n, 2, 64)).astype(np.float32), torch.bfloat16) for _ in range(2))
         good, gl = M.misa_prompt_attention(q, k, v, cuda(cu), want_lse=True)
         k[at], v[at, 0] = junk, junk
