@@ -7,23 +7,35 @@
 // (4096 multiply-adds a clock and SM), and as much time again for the pair's exponential (16 a clock and
 // SM): a 128 x 128 piece takes 2 x 512 clocks of products at d = 128 and 1024 of exponentials.  So a CTA
 // works on two tiles of 128 queries at once: while one tile's scores go through the softmax, the tensor
-// cores multiply for the other.
+// cores multiply for the other.  Measured, a pair of pieces takes 3250 clocks where the products alone
+// would take 2048: Q K^T runs at 600 to 700 clocks for 512 (both operands come from shared memory, 128
+// bytes a clock, all it has), and a tile's own chain (scores, weights, P V, the next Q K^T) is as long as
+// that, because tensor memory has no room for a second set of scores.  4096 queries ending 32768 keys (16
+// heads on 2): 840 us, 1230 TFLOP/s, 0.74 of the measured bf16 rate.
+// Tried and slower: scores of 64 keys in two halves, two steps ahead (1139 us for 838); a quarter to half
+// of the exponentials by a polynomial on the multiply-add units (860 to 927 for 858); reading the scores
+// twice from tensor memory instead of holding them (1073 for 1055); outputs through TMA stores.
 //
-// Per CTA (one per SM): 256 queries of one head, tiles A and B, and the keys they see in ascending
+// Per CTA (one per SM): items of 256 queries of one head, tiles A and B, and the keys they see in ascending
 // blocks of 128.  S = Q K^T and O += P V run on tcgen05 with fp32 accumulators in tensor memory
 // (S_A, S_B, O_A, O_B: 128 columns each, all 512); P overwrites the first half of its S as bf16, the A
 // operand of the second product.  Warp roles:
 //   warps 0-3, 4-7  softmax of tile A, B: one thread a query row, so row maxima and sums need no
 //                   exchange; also rescale O, normalise and write the output
 //   warp 8          TMA producer: the two Q tiles, then K and V blocks through a ring of buffers
-//   warp 9          MMA issuer (one thread) and owner of the tensor memory
+//   warp 9          MMA issuer (one elected thread) and owner of the tensor memory
 //   warps 10, 11    guards: in the blocks where some query does not see every key they set to zero the
 //                   value rows behind the sequence and every value that is not finite (a weight of
 //                   zero times such a value would not be zero), before the product reads them
 // The running maximum m is raised, and O rescaled, only when a row's scores pass it by 8 (base 2): O and
 // the sum stay right for any m, and weights up to 2^8 lose nothing in bf16 or fp32.  Weights are rounded
-// to bf16 (2^-9) for the product with V, of the same type; their sum is taken before, in fp32.
-// Values that are not finite and were set to zero are added to the rows that do see them at the end.
+// to bf16 (half a step, 2^-8 of the weight) for the product with V, of the same type; their sum is taken
+// before, in fp32.  Values that are not finite and were set to zero are added to the rows that do see
+// them at the end.
+//
+// Which CTA does what: with many items one CTA takes one item, and the GPU's own dispatch evens them out;
+// with few, or few long ones, 148 CTAs share the items' blocks equally, an item that a boundary cuts is
+// left in pieces, and a last kernel joins them (130 queries over 20000 keys keep every SM busy).
 // Every wait is bounded in time; a wait that runs out sets a device status word and all roles leave
 // their loops, wait for their own copies and MMAs, and free tensor memory.
 #include <cuda.h>
@@ -123,8 +135,9 @@ struct Plan {
 };
 
 // An item costs its blocks and what its start and end take, in blocks.
-constexpr int kItemCost = 2;
+constexpr int kItemCost = 4;
 constexpr int kCtas = 148;
+constexpr int64_t kManyItems = 4 * kCtas;
 
 struct PromptArgs {
   const __nv_bfloat16* v;
@@ -518,380 +531,380 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t done = 0;  // blocks of this tile so far
     for (int seg = 0;; ++seg) {
-    const int from = walk.from(t), to_ = walk.to(t);
-    float m = -INFINITY, l = 0.f;  // maximum of the raw scores, sum of the weights
-    for (int j = from; j < to_; ++j, ++done) {
-      if (!wait_for(sfull(t), done & 1, abort)) {
-        ok = false;
-        break;
-      }
-      tc::tc_fence_after();
-      uint32_t s[4][32];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) tc::tmem_ld32(ts + 32 * x, s[x]);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) tc::tmem_ld_wait(s[x]);
-      if (walk.p.masked(t, j)) {
-        const int seen = min(walk.p.keys, i + walk.p.off + 1) - j * kRows;  // keys of this block that row i sees
-#pragma unroll
-        for (int x = 0; x < 4; ++x) hide(s[x], seen - 32 * x);
-      }
-      // Weights go pair by pair through multiply-add, exponential, and kLag pairs later sum and rounding, so
-      // that the exponentials (8 clocks a warp and instruction) never wait for their own results; 16 pairs
-      // are written at a time, over scores that have been read.  They start from the running maximum as it
-      // is, while the block's own maximum is found among the first 16 pairs' exponentials; should that pass
-      // it, these pairs are done again.
-      float2 sum[2], w[kLag];
-      uint32_t p[16];
-      float neg = m == -INFINITY ? 0.f : -m * c;
-      sum[0] = sum[1] = make_float2(0.f, 0.f);
-      auto start = [&](int e) {  // exponentials of pair e
-        const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[e / 16][2 * (e % 16)]), __uint_as_float(s[e / 16][2 * (e % 16) + 1])),
-                                    make_float2(c, c), make_float2(neg, neg));
-        w[e % kLag] = make_float2(ex2(z.x), ex2(z.y));
-      };
-      auto finish = [&](int e) {  // its sum and its rounding
-        const float2 v = w[e % kLag];
-        sum[e & 1] = __fadd2_rn(sum[e & 1], v);
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-        p[e & 15] = *reinterpret_cast<const uint32_t*>(&h);
-      };
-      float top[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) top[x] = __uint_as_float(s[x][0]);
-#pragma unroll
-      for (int e = 0; e < 16 + kLag; ++e) {
-        if (e >= kLag) finish(e - kLag);
-        if (e < 16) {
-          start(e);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) top[x] = max3(top[x], __uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1]));
+      const int from = walk.from(t), to_ = walk.to(t);
+      float m = -INFINITY, l = 0.f;  // maximum of the raw scores, sum of the weights
+      for (int j = from; j < to_; ++j, ++done) {
+        if (!wait_for(sfull(t), done & 1, abort)) {
+          ok = false;
+          break;
         }
-      }
-      const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
-      const bool raise = mx * c > m * c + kSlack;  // also the first score that is seen
-      if (__any_sync(0xffffffffu, raise)) {
-        if (j > from) {
-          // O holds the blocks before this one once their product is through
-          if (!wait_for(odone(t), (done - 1) & 1, abort)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const float f = raise && m != -INFINITY ? ex2((m - mx) * c) : 1.f;
-          l *= f;
-#pragma unroll 1
-          for (int x = 0; x < D; x += 8) {
-            uint32_t o[8];
-            tmem_ld8(to + x, o);
+        tc::tc_fence_after();
+        uint32_t s[4][32];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st8(to + x, o);
-          }
+        for (int x = 0; x < 4; ++x) tc::tmem_ld32(ts + 32 * x, s[x]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tc::tmem_ld_wait(s[x]);
+        if (walk.p.masked(t, j)) {
+          const int seen = min(walk.p.keys, i + walk.p.off + 1) - j * kRows;  // keys of this block that row i sees
+#pragma unroll
+          for (int x = 0; x < 4; ++x) hide(s[x], seen - 32 * x);
         }
-        if (raise) m = mx;
-        neg = m == -INFINITY ? 0.f : -m * c;
+        // Weights go pair by pair through multiply-add, exponential, and kLag pairs later sum and rounding, so
+        // that the exponentials (8 clocks a warp and instruction) never wait for their own results; 16 pairs
+        // are written at a time, over scores that have been read.  They start from the running maximum as it
+        // is, while the block's own maximum is found among the first 16 pairs' exponentials; should that pass
+        // it, these pairs are done again.
+        float2 sum[2], w[kLag];
+        uint32_t p[16];
+        float neg = m == -INFINITY ? 0.f : -m * c;
         sum[0] = sum[1] = make_float2(0.f, 0.f);
+        auto start = [&](int e) {  // exponentials of pair e
+          const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[e / 16][2 * (e % 16)]), __uint_as_float(s[e / 16][2 * (e % 16) + 1])),
+                                      make_float2(c, c), make_float2(neg, neg));
+          w[e % kLag] = make_float2(ex2(z.x), ex2(z.y));
+        };
+        auto finish = [&](int e) {  // its sum and its rounding
+          const float2 v = w[e % kLag];
+          sum[e & 1] = __fadd2_rn(sum[e & 1], v);
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+          p[e & 15] = *reinterpret_cast<const uint32_t*>(&h);
+        };
+        float top[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top[x] = __uint_as_float(s[x][0]);
 #pragma unroll
         for (int e = 0; e < 16 + kLag; ++e) {
           if (e >= kLag) finish(e - kLag);
-          if (e < 16) start(e);
-        }
-      }
-      tmem_st16(ts, p);
+          if (e < 16) {
+            start(e);
 #pragma unroll
-      for (int e = 16; e < 64 + kLag; ++e) {
-        if (e >= 16 + kLag) {
-          const int y = e - kLag;
-          finish(y);
-          if ((y & 15) == 15) tmem_st16(ts + y - 15, p);
-          if (y == 31) {  // half of the weights are there: their product may start
-            tmem_st_wait();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_relaxed(phalf(t));
+            for (int x = 0; x < 4; ++x) top[x] = max3(top[x], __uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1]));
           }
         }
-        if (e < 64) start(e);
-      }
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      tmem_st_wait();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive_relaxed(pfull(t));  // what it hands on lies in tensor memory
-    }
-    if (ok && to_ > from && !wait_for(odone(t), (done - 1) & 1, abort)) ok = false;
-    if (!ok) {
-      give_up(abort);
-      break;
-    }
-    tc::tc_fence_after();
-    const Pair& p = walk.p;
-    const bool whole = walk.whole();
-    if (t * kRows + (warp & 3) * 32 < p.rows || to_ > from) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int slot = 2 * blockIdx.x + (walk.j0 == 0 ? 1 : 0);
-      __nv_bfloat16* out = a.out + ((int64_t)(p.row + i) * a.Hq + walk.head) * D;
-      float* part = a.plan.part + (int64_t)slot * D * kPair + i;
-      // eight outputs at a time, in a loop of few instructions: once an item, this code is not in the
-      // instruction cache when it runs
+        const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+        const bool raise = mx * c > m * c + kSlack;  // also the first score that is seen
+        if (__any_sync(0xffffffffu, raise)) {
+          if (j > from) {
+            // O holds the blocks before this one once their product is through
+            if (!wait_for(odone(t), (done - 1) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            tc::tc_fence_after();
+            const float f = raise && m != -INFINITY ? ex2((m - mx) * c) : 1.f;
+            l *= f;
 #pragma unroll 1
-      for (int x = 0; x < D; x += 8) {
-        uint32_t o[8];
-        if (to_ > from) {
-          tmem_ld8(to + x, o);
-        } else {
+            for (int x = 0; x < D; x += 8) {
+              uint32_t o[8];
+              tmem_ld8(to + x, o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = 0u;
-        }
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) part[(x + e) * kPair] = __uint_as_float(o[e]);
-        } else {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+              for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st8(to + x, o);
+            }
           }
-          if (i < p.rows) *reinterpret_cast<uint4*>(out + x) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (raise) m = mx;
+          neg = m == -INFINITY ? 0.f : -m * c;
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 16 + kLag; ++e) {
+            if (e >= kLag) finish(e - kLag);
+            if (e < 16) start(e);
+          }
         }
-      }
-      if (to_ > from) {  // the next segment may overwrite O
+        tmem_st16(ts, p);
+#pragma unroll
+        for (int e = 16; e < 64 + kLag; ++e) {
+          if (e >= 16 + kLag) {
+            const int y = e - kLag;
+            finish(y);
+            if ((y & 15) == 15) tmem_st16(ts + y - 15, p);
+            if (y == 31) {  // half of the weights are there: their product may start
+              tmem_st_wait();
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive_relaxed(phalf(t));
+            }
+          }
+          if (e < 64) start(e);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_relaxed(oread(t));
+        if (lane == 0) tc::mbar_arrive_relaxed(pfull(t));  // what it hands on lies in tensor memory
       }
-      if (!whole) {
-        a.plan.part_ml[(slot * 2) * kPair + i] = m;
-        a.plan.part_ml[(slot * 2 + 1) * kPair + i] = l;
-      } else if (a.lse && i < p.rows) {
-        a.lse[((int64_t)p.row + i) * a.Hq + walk.head] = l == 0.f ? -INFINITY : m * c * 0.693147180559945309f + logf(l);
-      }
-      if (odd[seg & 3] == seg + 1 && i < p.rows)
-        add_strange<D>(a.v + (int64_t)p.key0 * a.ldv + (walk.head / a.G) * D, a.ldv, p, from, to_, i,
-                       whole ? out : nullptr, part);
-    }
-    if (!walk.advance(a)) break;
-    }
-  } else {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-  if (warp == kLoadWarp) {
-    // ---------------- TMA producer ----------------
-    if (elect_one()) {
-      bool ok = true;
-      uint32_t u = 0, q[2] = {0, 0};  // ring buffers and Q tiles filled so far
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok && !wait_for(bar, parity, abort)) ok = false;
-        return ok;
-      };
-      do {
-        const Pair& p = walk.p;
-        const int hk = walk.head / a.G;
-        const bool has[2] = {walk.to(0) > walk.from(0), walk.to(1) > walk.from(1)};
-        auto q_tile = [&](int t) {
-          if (q[t] > 0 && !wait(qempty(t), (q[t] - 1) & 1)) return;
-          ++q[t];
-          tc::mbar_arrive_expect_tx(qfull(t), L::kTileBytes);
-#pragma unroll
-          for (int x = 0; x < D / 64; ++x)
-            tc::tma_load_2d(qbase + t * L::kTileBytes + x * L::kHalfBytes, &qmap, walk.head * D + x * 64,
-                            p.row + t * kRows, qfull(t));
-        };
-        const int j1 = max(walk.to(0), walk.to(1));
-        if (has[0]) q_tile(0);
-        for (int j = walk.j0; ok && j < j1; ++j) {
-          for (int side = 0; ok && side < 2; ++side, ++u) {
-            const int b = u % NB;
-            if (u >= NB && !wait(empty(b), ((u / NB) - 1) & 1)) break;
-            tc::mbar_arrive_expect_tx(full(b), L::kTileBytes);
-#pragma unroll
-            for (int x = 0; x < D / 64; ++x)
-              tc::tma_load_2d(ring + b * L::kTileBytes + x * L::kHalfBytes, side ? &vmap : &kmap, hk * D + x * 64,
-                              p.key0 + j * kRows, full(b));
-            if (j == walk.j0 && side == 0 && has[1]) q_tile(1);
-          }
-        }
-      } while (ok && walk.advance(a));
-      if (!ok) give_up(abort);
-      // every issued copy lands before the CTA exits
-      for (int t = 0; t < 2; ++t)
-        if (q[t] > 0) wait_for(qfull(t), (q[t] - 1) & 1, nullptr);
-      for (uint32_t g = u > NB ? u - NB : 0; g < u; ++g) wait_for(full(g % NB), (g / NB) & 1, nullptr);
-    }
-  } else if (warp == kMmaWarp) {
-    // ---------------- MMA issuer ----------------
-    if (elect_one()) {
-      constexpr uint32_t idesc_s = tc::idesc_bf16_f32(kRows, kRows);
-      constexpr uint32_t idesc_o = tc::idesc_bf16_f32(kRows, D) | (1u << 16);  // V with its dims contiguous
-      bool ok = true;
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok && !wait_for(bar, parity, abort)) ok = false;
-        return ok;
-      };
-      // One segment's blocks of either tile, [f0, t0) and [f1, t1), and the ring turn of its block j0
-      struct Seg {
-        int f0, t0, f1, t1, j0, j1;
-        uint32_t turn;
-        __device__ __forceinline__ int from(int t) const { return t ? f1 : f0; }
-        __device__ __forceinline__ int to(int t) const { return t ? t1 : t0; }
-        // the last tile that reads block j
-        __device__ __forceinline__ bool last(int t, int j) const { return t == 1 || j < f1 || j >= t1; }
-      };
-      auto segment = [&](uint32_t turn) {
-        Seg g;
-        g.f0 = walk.from(0);
-        g.t0 = walk.to(0);
-        g.f1 = walk.from(1);
-        g.t1 = walk.to(1);
-        g.j0 = walk.j0;
-        g.j1 = max(g.t0, g.t1);
-        g.turn = turn;
-        return g;
-      };
-      uint32_t qn0 = 0, qn1 = 0, on0 = 0, on1 = 0, dn0 = 0, dn1 = 0;  // Q tiles, outputs and blocks begun, by tile
-      auto scores = [&](const Seg& g, const int t, int j) {  // S_t = Q_t K_j^T
-        const uint32_t u = g.turn + 2 * (j - g.j0), b = u % NB;
-        if (j == g.from(t)) {
-          uint32_t& qn = t ? qn1 : qn0;
-          if (!wait(qfull(t), qn & 1)) return;
-          ++qn;
-        }
-        if (!wait(full(b), (u / NB) & 1)) return;
-        const uint64_t qd = tc::sw128_kmajor_desc(qbase + t * L::kTileBytes), kd = tc::sw128_kmajor_desc(ring + b * L::kTileBytes);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = ((kk / 4) * L::kHalfBytes + (kk % 4) * 32) >> 4;
-          tc::mma_bf16(tmem + t * kRows, qd + at, kd + at, idesc_s, kk != 0);
-        }
-        tc::mma_commit(sfull(t));
-        if (j + 1 == g.to(t)) tc::mma_commit(qempty(t));
-        if (g.last(t, j)) tc::mma_commit(empty(b));
-      };
-      auto values = [&](const Seg& g, const int t, int j) {  // O_t += P_t V_j
-        const uint32_t u = g.turn + 2 * (j - g.j0) + 1, b = u % NB;
-        uint32_t& dn = t ? dn1 : dn0;
-        if (!wait(vok(b), (u / NB) & 1)) return;
-        if (j == g.from(t)) {
-          uint32_t& on = t ? on1 : on0;
-          if (on > 0 && !wait(oread(t), (on - 1) & 1)) return;
-          ++on;
-        }
-        const uint64_t vd = sw128_mnmajor_desc(ring + b * L::kTileBytes, L::kHalfBytes);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (!wait(half ? pfull(t) : phalf(t), dn & 1)) return;
-          tc::tc_fence_after();  // after the weights' stores to tensor memory, by other threads
-#pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            mma_bf16_ts(tmem + 2 * kRows + t * kRows, tmem + t * kRows + kk * 8, vd + kk * (2048 >> 4), idesc_o,
-                        (j > g.from(t)) || kk != 0);
-        }
-        tc::mma_commit(odone(t));
-        if (g.last(t, j)) tc::mma_commit(empty(b));
-        ++dn;
-      };
-      Seg g = segment(0);
-      if (g.t0 > g.f0) scores(g, 0, g.f0);
-      if (ok && g.t1 > g.f1) scores(g, 1, g.f1);
-      while (ok) {
-        const bool more = walk.advance(a);
-        Seg next = g;
-        if (more) next = segment(g.turn + 2 * (uint32_t)max(0, g.j1 - g.j0));
-        // a tile's first scores of the next segment follow its last block of this one, unless the other tile
-        // has more than one block to go: the ring could not hold what lies between
-        bool begun0 = false, begun1 = false;
-        for (int j = g.j0; ok && j < g.j1; ++j) {
-          const bool ahead = more && j + 2 >= g.j1;
-          if (j >= g.f0 && j < g.t0) {
-            values(g, 0, j);
-            if (ok && j + 1 < g.t0) {
-              scores(g, 0, j + 1);
-            } else if (ok && ahead && next.t0 > next.f0) {
-              scores(next, 0, next.f0);
-              begun0 = true;
-            }
-          }
-          if (ok && j >= g.f1 && j < g.t1) {
-            values(g, 1, j);
-            if (ok && j + 1 < g.t1) {
-              scores(g, 1, j + 1);
-            } else if (ok && ahead && j + 1 == g.j1 && next.t1 > next.f1 && (begun0 || next.t0 <= next.f0)) {
-              // (behind the first tile's: the second one's use of a block is taken to be the last)
-              scores(next, 1, next.f1);
-              begun1 = true;
-            }
-          }
-        }
-        if (!ok || !more) break;
-        g = next;
-        if (!begun0 && g.t0 > g.f0) scores(g, 0, g.f0);
-        if (ok && !begun1 && g.t1 > g.f1) scores(g, 1, g.f1);
-      }
-      if (!ok) give_up(abort);
-      // every issued MMA completes before tensor memory is freed
-      tc::mma_commit(drain);
-      wait_for(drain, 0, nullptr);
-    }
-  } else {
-    // ---------------- guards ----------------
-    bool ok = true;
-    uint32_t u = 1;  // ring turn of the next V
-    for (int seg = 0;; ++seg) {
-    for (int j = walk.j0; ok && j < max(walk.to(0), walk.to(1)); ++j, u += 2) {
-      const uint32_t b = u % NB;
-      if (!wait_for(full(b), (u / NB) & 1, abort)) {
-        ok = false;
+      if (ok && to_ > from && !wait_for(odone(t), (done - 1) & 1, abort)) ok = false;
+      if (!ok) {
+        give_up(abort);
         break;
       }
-      if (!walk.guarded(j)) {  // passed on all the same: a guard that fell behind by a turn of the ring would miss its phase
-        if (lane == 0) tc::mbar_arrive(vok(b));
-        continue;
-      }
-      const int there = walk.p.keys - j * kRows;  // rows from here on belong to no key of the sequence
-      const int first = (warp - kGuardWarp) * (kRows / 2);
-      uint8_t* v = sm + L::kOffRing + b * L::kTileBytes;
-      // a 16-bit number whose exponent is all ones carries into its top bit
-      auto hit = [](uint32_t z) { return ((z & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
-      auto clean = [&](uint32_t z) { return z & ~((hit(z) >> 15) * 0xffffu); };
-      constexpr int kPieces = (kRows / 2) * (D / 8);  // of 16 bytes, 8 a row and box of 64 dims
-      auto piece = [&](int x) {
-        const int half = x / (kRows / 2 * 8), y = x % (kRows / 2 * 8);
-        return reinterpret_cast<uint4*>(v + half * L::kHalfBytes + (first + y / 8) * 128 + (y % 8) * 16);
-      };
-      bool changed = false, bad = false;
-      if (first + kRows / 2 > there) {
-        for (int x = lane; x < kPieces; x += 32)
-          if (first + x % (kRows / 2 * 8) / 8 >= there) *piece(x) = make_uint4(0u, 0u, 0u, 0u);
-        changed = true;
-      }
+      tc::tc_fence_after();
+      const Pair& p = walk.p;
+      const bool whole = walk.whole();
+      if (t * kRows + (warp & 3) * 32 < p.rows || to_ > from) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int slot = 2 * blockIdx.x + (walk.j0 == 0 ? 1 : 0);
+        __nv_bfloat16* out = a.out + ((int64_t)(p.row + i) * a.Hq + walk.head) * D;
+        float* part = a.plan.part + (int64_t)slot * D * kPair + i;
+        // eight outputs at a time, in a loop of few instructions: once an item, this code is not in the
+        // instruction cache when it runs
 #pragma unroll 1
-      for (int x0 = lane; x0 < kPieces; x0 += 32 * 8) {
-        uint4 w[8];
+        for (int x = 0; x < D; x += 8) {
+          uint32_t o[8];
+          if (to_ > from) {
+            tmem_ld8(to + x, o);
+          } else {
 #pragma unroll
-        for (int y = 0; y < 8; ++y) w[y] = *piece(x0 + 32 * y);
-        uint32_t any = 0;
-#pragma unroll
-        for (int y = 0; y < 8; ++y) any |= hit(w[y].x) | hit(w[y].y) | hit(w[y].z) | hit(w[y].w);
-        if (any) {
-#pragma unroll 1
-          for (int y = 0; y < 8; ++y) {
-            uint4* p = piece(x0 + 32 * y);
-            const uint4 z = *p;
-            *p = make_uint4(clean(z.x), clean(z.y), clean(z.z), clean(z.w));
+            for (int e = 0; e < 8; ++e) o[e] = 0u;
           }
-          changed = bad = true;
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) part[(x + e) * kPair] = __uint_as_float(o[e]);
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+              w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            if (i < p.rows) *reinterpret_cast<uint4*>(out + x) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
+        if (to_ > from) {  // the next segment may overwrite O
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_relaxed(oread(t));
+        }
+        if (!whole) {
+          a.plan.part_ml[(slot * 2) * kPair + i] = m;
+          a.plan.part_ml[(slot * 2 + 1) * kPair + i] = l;
+        } else if (a.lse && i < p.rows) {
+          a.lse[((int64_t)p.row + i) * a.Hq + walk.head] = l == 0.f ? -INFINITY : m * c * 0.693147180559945309f + logf(l);
+        }
+        if (odd[seg & 3] == seg + 1 && i < p.rows)
+          add_strange<D>(a.v + (int64_t)p.key0 * a.ldv + (walk.head / a.G) * D, a.ldv, p, from, to_, i,
+                         whole ? out : nullptr, part);
       }
-      if (bad) odd[seg & 3] = seg + 1;
-      if (changed) tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(vok(b));
+      if (!walk.advance(a)) break;
     }
-    if (!ok || !walk.advance(a)) break;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    if (warp == kLoadWarp) {
+      // ---------------- TMA producer ----------------
+      if (elect_one()) {
+        bool ok = true;
+        uint32_t u = 0, q[2] = {0, 0};  // ring buffers and Q tiles filled so far
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          if (ok && !wait_for(bar, parity, abort)) ok = false;
+          return ok;
+        };
+        do {
+          const Pair& p = walk.p;
+          const int hk = walk.head / a.G;
+          const bool has[2] = {walk.to(0) > walk.from(0), walk.to(1) > walk.from(1)};
+          auto q_tile = [&](int t) {
+            if (q[t] > 0 && !wait(qempty(t), (q[t] - 1) & 1)) return;
+            ++q[t];
+            tc::mbar_arrive_expect_tx(qfull(t), L::kTileBytes);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              tc::tma_load_2d(qbase + t * L::kTileBytes + x * L::kHalfBytes, &qmap, walk.head * D + x * 64,
+                              p.row + t * kRows, qfull(t));
+          };
+          const int j1 = max(walk.to(0), walk.to(1));
+          if (has[0]) q_tile(0);
+          for (int j = walk.j0; ok && j < j1; ++j) {
+            for (int side = 0; ok && side < 2; ++side, ++u) {
+              const int b = u % NB;
+              if (u >= NB && !wait(empty(b), ((u / NB) - 1) & 1)) break;
+              tc::mbar_arrive_expect_tx(full(b), L::kTileBytes);
+#pragma unroll
+              for (int x = 0; x < D / 64; ++x)
+                tc::tma_load_2d(ring + b * L::kTileBytes + x * L::kHalfBytes, side ? &vmap : &kmap, hk * D + x * 64,
+                                p.key0 + j * kRows, full(b));
+              if (j == walk.j0 && side == 0 && has[1]) q_tile(1);
+            }
+          }
+        } while (ok && walk.advance(a));
+        if (!ok) give_up(abort);
+        // every issued copy lands before the CTA exits
+        for (int t = 0; t < 2; ++t)
+          if (q[t] > 0) wait_for(qfull(t), (q[t] - 1) & 1, nullptr);
+        for (uint32_t g = u > NB ? u - NB : 0; g < u; ++g) wait_for(full(g % NB), (g / NB) & 1, nullptr);
+      }
+    } else if (warp == kMmaWarp) {
+      // ---------------- MMA issuer ----------------
+      if (elect_one()) {
+        constexpr uint32_t idesc_s = tc::idesc_bf16_f32(kRows, kRows);
+        constexpr uint32_t idesc_o = tc::idesc_bf16_f32(kRows, D) | (1u << 16);  // V with its dims contiguous
+        bool ok = true;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+          if (ok && !wait_for(bar, parity, abort)) ok = false;
+          return ok;
+        };
+        // One segment's blocks of either tile, [f0, t0) and [f1, t1), and the ring turn of its block j0
+        struct Seg {
+          int f0, t0, f1, t1, j0, j1;
+          uint32_t turn;
+          __device__ __forceinline__ int from(int t) const { return t ? f1 : f0; }
+          __device__ __forceinline__ int to(int t) const { return t ? t1 : t0; }
+          // the last tile that reads block j
+          __device__ __forceinline__ bool last(int t, int j) const { return t == 1 || j < f1 || j >= t1; }
+        };
+        auto segment = [&](uint32_t turn) {
+          Seg g;
+          g.f0 = walk.from(0);
+          g.t0 = walk.to(0);
+          g.f1 = walk.from(1);
+          g.t1 = walk.to(1);
+          g.j0 = walk.j0;
+          g.j1 = max(g.t0, g.t1);
+          g.turn = turn;
+          return g;
+        };
+        uint32_t qn0 = 0, qn1 = 0, on0 = 0, on1 = 0, dn0 = 0, dn1 = 0;  // Q tiles, outputs and blocks begun, by tile
+        auto scores = [&](const Seg& g, const int t, int j) {  // S_t = Q_t K_j^T
+          const uint32_t u = g.turn + 2 * (j - g.j0), b = u % NB;
+          if (j == g.from(t)) {
+            uint32_t& qn = t ? qn1 : qn0;
+            if (!wait(qfull(t), qn & 1)) return;
+            ++qn;
+          }
+          if (!wait(full(b), (u / NB) & 1)) return;
+          const uint64_t qd = tc::sw128_kmajor_desc(qbase + t * L::kTileBytes), kd = tc::sw128_kmajor_desc(ring + b * L::kTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = ((kk / 4) * L::kHalfBytes + (kk % 4) * 32) >> 4;
+            tc::mma_bf16(tmem + t * kRows, qd + at, kd + at, idesc_s, kk != 0);
+          }
+          tc::mma_commit(sfull(t));
+          if (j + 1 == g.to(t)) tc::mma_commit(qempty(t));
+          if (g.last(t, j)) tc::mma_commit(empty(b));
+        };
+        auto values = [&](const Seg& g, const int t, int j) {  // O_t += P_t V_j
+          const uint32_t u = g.turn + 2 * (j - g.j0) + 1, b = u % NB;
+          uint32_t& dn = t ? dn1 : dn0;
+          if (!wait(vok(b), (u / NB) & 1)) return;
+          if (j == g.from(t)) {
+            uint32_t& on = t ? on1 : on0;
+            if (on > 0 && !wait(oread(t), (on - 1) & 1)) return;
+            ++on;
+          }
+          const uint64_t vd = sw128_mnmajor_desc(ring + b * L::kTileBytes, L::kHalfBytes);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!wait(half ? pfull(t) : phalf(t), dn & 1)) return;
+            tc::tc_fence_after();  // after the weights' stores to tensor memory, by other threads
+#pragma unroll
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              mma_bf16_ts(tmem + 2 * kRows + t * kRows, tmem + t * kRows + kk * 8, vd + kk * (2048 >> 4), idesc_o,
+                          (j > g.from(t)) || kk != 0);
+          }
+          tc::mma_commit(odone(t));
+          if (g.last(t, j)) tc::mma_commit(empty(b));
+          ++dn;
+        };
+        Seg g = segment(0);
+        if (g.t0 > g.f0) scores(g, 0, g.f0);
+        if (ok && g.t1 > g.f1) scores(g, 1, g.f1);
+        while (ok) {
+          const bool more = walk.advance(a);
+          Seg next = g;
+          if (more) next = segment(g.turn + 2 * (uint32_t)max(0, g.j1 - g.j0));
+          // a tile's first scores of the next segment follow its last block of this one, unless the other tile
+          // has more than one block to go: the ring could not hold what lies between
+          bool begun0 = false, begun1 = false;
+          for (int j = g.j0; ok && j < g.j1; ++j) {
+            const bool ahead = more && j + 2 >= g.j1;
+            if (j >= g.f0 && j < g.t0) {
+              values(g, 0, j);
+              if (ok && j + 1 < g.t0) {
+                scores(g, 0, j + 1);
+              } else if (ok && ahead && next.t0 > next.f0) {
+                scores(next, 0, next.f0);
+                begun0 = true;
+              }
+            }
+            if (ok && j >= g.f1 && j < g.t1) {
+              values(g, 1, j);
+              if (ok && j + 1 < g.t1) {
+                scores(g, 1, j + 1);
+              } else if (ok && ahead && j + 1 == g.j1 && next.t1 > next.f1 && (begun0 || next.t0 <= next.f0)) {
+                // (behind the first tile's: the second one's use of a block is taken to be the last)
+                scores(next, 1, next.f1);
+                begun1 = true;
+              }
+            }
+          }
+          if (!ok || !more) break;
+          g = next;
+          if (!begun0 && g.t0 > g.f0) scores(g, 0, g.f0);
+          if (ok && !begun1 && g.t1 > g.f1) scores(g, 1, g.f1);
+        }
+        if (!ok) give_up(abort);
+        // every issued MMA completes before tensor memory is freed
+        tc::mma_commit(drain);
+        wait_for(drain, 0, nullptr);
+      }
+    } else {
+      // ---------------- guards ----------------
+      bool ok = true;
+      uint32_t u = 1;  // ring turn of the next V
+      for (int seg = 0;; ++seg) {
+        for (int j = walk.j0; ok && j < max(walk.to(0), walk.to(1)); ++j, u += 2) {
+          const uint32_t b = u % NB;
+          if (!wait_for(full(b), (u / NB) & 1, abort)) {
+            ok = false;
+            break;
+          }
+          if (!walk.guarded(j)) {  // passed on all the same: a guard that fell behind by a turn of the ring would miss its phase
+            if (lane == 0) tc::mbar_arrive(vok(b));
+            continue;
+          }
+          const int there = walk.p.keys - j * kRows;  // rows from here on belong to no key of the sequence
+          const int first = (warp - kGuardWarp) * (kRows / 2);
+          uint8_t* v = sm + L::kOffRing + b * L::kTileBytes;
+          // a 16-bit number whose exponent is all ones carries into its top bit
+          auto hit = [](uint32_t z) { return ((z & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+          auto clean = [&](uint32_t z) { return z & ~((hit(z) >> 15) * 0xffffu); };
+          constexpr int kPieces = (kRows / 2) * (D / 8);  // of 16 bytes, 8 a row and box of 64 dims
+          auto piece = [&](int x) {
+            const int half = x / (kRows / 2 * 8), y = x % (kRows / 2 * 8);
+            return reinterpret_cast<uint4*>(v + half * L::kHalfBytes + (first + y / 8) * 128 + (y % 8) * 16);
+          };
+          bool changed = false, bad = false;
+          if (first + kRows / 2 > there) {
+            for (int x = lane; x < kPieces; x += 32)
+              if (first + x % (kRows / 2 * 8) / 8 >= there) *piece(x) = make_uint4(0u, 0u, 0u, 0u);
+            changed = true;
+          }
+#pragma unroll 1
+          for (int x0 = lane; x0 < kPieces; x0 += 32 * 8) {
+            uint4 w[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) w[y] = *piece(x0 + 32 * y);
+            uint32_t any = 0;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) any |= hit(w[y].x) | hit(w[y].y) | hit(w[y].z) | hit(w[y].w);
+            if (any) {
+#pragma unroll 1
+              for (int y = 0; y < 8; ++y) {
+                uint4* p = piece(x0 + 32 * y);
+                const uint4 z = *p;
+                *p = make_uint4(clean(z.x), clean(z.y), clean(z.z), clean(z.w));
+              }
+              changed = bad = true;
+            }
+          }
+          if (bad) odd[seg & 3] = seg + 1;
+          if (changed) tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(vok(b));
+        }
+        if (!ok || !walk.advance(a)) break;
+      }
+      if (!ok) give_up(abort);
     }
-    if (!ok) give_up(abort);
-  }
   }
 
   tc::tc_fence_before();
@@ -960,9 +973,13 @@ bool row_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int
 
 int64_t most_pairs(int S, int Tq) { return (int64_t)Tq / kPair + std::min(S, Tq); }
 
-// Whether a call goes without a plan, one item a CTA: few enough items for one CTA an SM, none of them long
-// (32 blocks of keys at most), so that cutting them up would not pay for the two launches it adds.
-bool plain_call(int S, int Tq, int Tk, int Hq) { return most_pairs(S, Tq) * Hq <= kCtas && Tk <= 32 * kRows; }
+// Whether a call goes without a plan, one item a CTA: where the items are few enough for one CTA an SM and
+// none is long (32 blocks of keys at most), so that cutting them up would not pay for the two launches it
+// adds, and where they are many, so that the GPU's own dispatch evens them out.
+bool plain_call(int S, int Tq, int Tk, int Hq) {
+  const int64_t items = most_pairs(S, Tq) * Hq;
+  return items > kManyItems || (items <= kCtas && Tk <= 32 * kRows);
+}
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 

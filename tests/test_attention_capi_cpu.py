@@ -102,7 +102,7 @@ def test_prompt_refusals(lib):
                      (dict(scale=-0.1), INVALID), (dict(scale=INF), INVALID), (dict(q=None), INVALID), (dict(k=BENT), INVALID),
                      (dict(ldq=4092), INVALID), (dict(ldk=1016), INVALID), (dict(ldv=1027), INVALID), (dict(out=None), INVALID),
                      (dict(out=BENT), INVALID), (dict(cuq=None), INVALID), (dict(cuk=None), INVALID),
-                     (dict(Tq=9000, ws=None), WORKSPACE), (dict(Tq=9000, ws=BENT), WORKSPACE), (dict(Tq=9000, wsb=1000), WORKSPACE),
+                     (dict(Tk=9000, ws=None), WORKSPACE), (dict(Tk=9000, ws=BENT), WORKSPACE), (dict(Tk=9000, wsb=1000), WORKSPACE),
                      (dict(Tq=0, q=None, out=None), OK), (dict(S=0, cuq=None), OK)]:
         assert call(lib.misa_prompt_attention, PROMPT, **kw) == want, kw
 

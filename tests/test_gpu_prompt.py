@@ -81,7 +81,7 @@ def test_longer_prompts(d):
     (128, 4, 2, [130], [20000]),                     # two items a head, cut between all CTAs
     (64, 2, 1, [1], [9000]),
     (128, 1, 1, [300, 1, 257], [5000, 0, -200]),     # items of every length, some queries before the first key
-    (64, 24, 8, [400, 0, 90, 1, 700, 256, 33] * 3, [0] * 21),   # more items than CTAs
+    (64, 24, 8, [400, 0, 90, 1, 700, 256, 33] * 3, [0] * 21),   # more items than are cut
     (128, 16, 2, [64] * 60 + [900], [0] * 60 + [3000]),
 ])
 def test_items_cut_between_ctas(d, Hq, Hkv, lens, extra):
@@ -90,7 +90,6 @@ def test_items_cut_between_ctas(d, Hq, Hkv, lens, extra):
     cu_q, cu_k = cum(lens), cum([a + b for a, b in zip(lens, extra)])
     q = cuda(rng.standard_normal((cu_q[-1], Hq, d)).astype(np.float32) * 2, torch.bfloat16)
     k, v = (cuda(rng.standard_normal((cu_k[-1], Hkv, d)).astype(np.float32), torch.bfloat16) for _ in range(2))
-    assert M.misa_workspace_bytes(M.OP_PROMPT_ATTENTION, int(cu_q[-1]), int(cu_k[-1]), Hq, len(lens), d) > 0
     out, lse = M.misa_prompt_attention(q, k, v, cuda(cu_q), cuda(cu_k), want_lse=True)
     check(M, q, k, v, cu_q, cu_k, out, lse, d ** -0.5, rows=12)
     again, al = M.misa_prompt_attention(q, k, v, cuda(cu_q), cuda(cu_k), want_lse=True)
