@@ -627,32 +627,57 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(8 * NT)) kv4_attn_kern
   }
 }
 
-// Joins the pieces of a (query, head) whose tokens more than one CTA took; also writes the heads of
-// queries that attend to nothing.  One CTA per head: its threads first weigh the pieces (each by its
-// maximum against the largest), then its warps add up every eighth piece.
-template <int D, int SPLIT>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a, int HB, int64_t ctas) {
-  constexpr int E = D / 32;  // output elements of a lane
-  __shared__ float weight[kMaxCtas];
-  __shared__ float red[8];
-  __shared__ __align__(16) float part[8][D];
-  pdl_wait();
-  const int hd = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = hd / a.Hq, hq = hd % a.Hq;
-  const int hk = hq / a.G, hr = hq % a.G, head = hr % HB;
+// The pieces of a (query, head): count 0 where it attends to nothing, 1 where one CTA had it whole (and has
+// written its output and log-sum), else the pieces lie in slots first, first + 1, ...
+struct Pieces {
+  int64_t first;
+  int count;
+};
+
+__device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, int t, int hq, int HB, int64_t ctas) {
+  const int hk = hq / a.G, hr = hq % a.G;
   const int items = a.pool.Hkv * a.groups, item = hk * a.groups + hr / HB;
   const uint64_t W = a.pre[a.T], first = a.pre[t];
   const uint64_t units = (a.pre[t + 1] - first) / items;
-  int pieces = 0;
-  int64_t slot0 = 0;
+  Pieces r = {0, 0};
   if (units > 0) {
     const uint64_t grid = W < (uint64_t)ctas ? W : (uint64_t)ctas;
     const uint64_t p0 = first + item * units, p1 = p0 + units;
     const int64_t c0 = (int64_t)(((p0 + 1) * grid - 1) / W), c1 = (int64_t)((p1 * grid - 1) / W);
-    if (c0 == c1) return;  // one CTA had the whole head
-    slot0 = c0 + (int64_t)t * items + item;
-    pieces = (int)(c1 - c0 + 1);
+    r.first = c0 + (int64_t)t * items + item;
+    r.count = (int)(c1 - c0 + 1);
   }
+  return r;
+}
+
+__device__ __forceinline__ float2 piece_ml(const AttnArgs& a, int64_t slot, int HB, int head) {
+  return *reinterpret_cast<const float2*>(a.part_ml + (slot * HB + head) * 2);
+}
+
+template <int SPLIT>
+__device__ __forceinline__ void store_out(const AttnArgs& a, int64_t at, float v) {
+  if (SPLIT == 1) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+  else static_cast<float*>(a.out)[at] = v;
+}
+
+__device__ __forceinline__ void store_lse(const AttnArgs& a, int64_t hd, float top, float sum) {
+  const float z = sum == 0.f ? -INFINITY : top + log2f(sum) - kLift;
+  if (a.lse) a.lse[hd] = z * 0.693147180559945309f;
+  if (a.lse2) a.lse2[hd] = z;
+}
+
+// The joins of one head by a whole CTA: its threads first weigh the pieces (each by its maximum against the
+// largest), then its warps add up every eighth piece.
+template <int D, int SPLIT>
+__device__ __forceinline__ void join_wide(const AttnArgs& a, int hd, int HB, int64_t ctas) {
+  constexpr int E = D / 32;  // output elements of a lane
+  __shared__ float weight[kMaxCtas];
+  __shared__ float red[8];
+  __shared__ __align__(16) float part[8][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int t = hd / a.Hq, hq = hd % a.Hq, head = hq % a.G % HB;
+  const Pieces pc = pieces_of(a, t, hq, HB, ctas);
+  if (pc.count == 1) return;
   auto over_block = [&](float v, bool largest) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -673,7 +698,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a, int HB,
 #pragma unroll
   for (int x = 0; x < kPer; ++x) {
     const int i = x * 256 + threadIdx.x;
-    ml[x] = i < pieces ? *reinterpret_cast<const float2*>(a.part_ml + ((slot0 + i) * HB + head) * 2) : make_float2(-INFINITY, 0.f);
+    ml[x] = i < pc.count ? piece_ml(a, pc.first + i, HB, head) : make_float2(-INFINITY, 0.f);
     top = fmaxf(top, ml[x].x);
   }
   top = over_block(top, true);
@@ -681,7 +706,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a, int HB,
   for (int x = 0; x < kPer; ++x) {
     const int i = x * 256 + threadIdx.x;
     const float f = ml[x].y == 0.f ? 0.f : exp2_fast(ml[x].x - top);
-    if (i < pieces) weight[i] = f;
+    if (i < pc.count) weight[i] = f;
     sum += f * ml[x].y;
   }
   sum = over_block(sum, false);
@@ -689,8 +714,8 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a, int HB,
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int i = warp; i < pieces; i += 8) {
-    const float* p = a.part + ((slot0 + i) * HB + head) * D + lane * E;
+  for (int i = warp; i < pc.count; i += 8) {
+    const float* p = a.part + ((pc.first + i) * HB + head) * D + lane * E;
     const float f = weight[i];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += f * p[e];
@@ -702,38 +727,85 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a, int HB,
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) v += part[w][threadIdx.x];
-    v *= sum == 0.f ? 0.f : a.v_scale / sum;
-    const int64_t at = (int64_t)hd * D + threadIdx.x;
-    if (SPLIT == 1) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
-    else static_cast<float*>(a.out)[at] = v;
+    store_out<SPLIT>(a, (int64_t)hd * D + threadIdx.x, v * (sum == 0.f ? 0.f : a.v_scale / sum));
   }
-  if (threadIdx.x == 0) {
-    const float z = sum == 0.f ? -INFINITY : top + log2f(sum) - kLift;
-    if (a.lse) a.lse[hd] = z * 0.693147180559945309f;
-    if (a.lse2) a.lse2[hd] = z;
+  if (threadIdx.x == 0) store_lse(a, hd, top, sum);
+}
+
+// The join of one head by a warp.
+template <int D, int SPLIT>
+__device__ __forceinline__ void join_narrow(const AttnArgs& a, int hd, int HB, int64_t ctas) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, t = hd / a.Hq, hq = hd % a.Hq, head = hq % a.G % HB;
+  const Pieces pc = pieces_of(a, t, hq, HB, ctas);
+  if (pc.count == 1) return;
+  float top = -INFINITY, sum = 0.f, acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int i = lane; i < pc.count; i += 32) top = fmaxf(top, piece_ml(a, pc.first + i, HB, head).x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll 4
+  for (int i = 0; i < pc.count; ++i) {
+    const float2 ml = piece_ml(a, pc.first + i, HB, head);
+    const float* p = a.part + ((pc.first + i) * HB + head) * D + lane * E;
+    const float f = ml.y == 0.f ? 0.f : exp2_fast(ml.x - top);
+    sum += f * ml.y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += f * p[e];
+  }
+  const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+#pragma unroll
+  for (int e = 0; e < E; ++e) store_out<SPLIT>(a, (int64_t)hd * D + lane * E + e, acc[e] * inv);
+  if (lane == 0) store_lse(a, hd, top, sum);
+}
+
+// Joins the pieces of a (query, head) whose tokens more than one CTA took; also writes the heads of queries that
+// attend to nothing.  WIDE: a CTA a head, else a warp.
+template <int D, int SPLIT, bool WIDE>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a, int HB, int64_t ctas) {
+  pdl_wait();
+  if (WIDE) {
+    join_wide<D, SPLIT>(a, blockIdx.x, HB, ctas);
+  } else {
+    const int hd = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (hd < a.T * a.Hq) join_narrow<D, SPLIT>(a, hd, HB, ctas);
   }
 }
 
-// acc[t, i] += sum over the heads of token i's weight, from the logits and every head's log-sum.
+// acc[t, i] += sum over the heads of token i's weight, from the logits and every head's log-sum.  SHARE threads
+// a position, each every SHARE-th head, and their sums in order.
 // Selected tokens are added atomically: a token that a list names twice gets both of its (equal)
 // weights, in either order the same sum.
+template <int SHARE>
 __global__ void __launch_bounds__(256) kv4_weights_kernel(const AttnArgs a, float* __restrict__ acc, int64_t ld) {
+  constexpr int kTokens = 256 / SHARE;
+  __shared__ float part[SHARE][kTokens];
   pdl_wait();
-  const int t = blockIdx.y;
-  const int p = blockIdx.x * 256 + threadIdx.x;
-  const int nt = clamp_len(a.n[t], a.L);
-  const int len = a.idx ? a.P : nt;
-  if (p >= len) return;
-  const int s = a.idx ? a.idx[(int64_t)t * a.P + p] : p;
-  if (s < 0 || s >= nt) return;
-  const float* row = a.logits + (int64_t)t * a.Hq * a.ldS + p;
-  const float* z = a.lse2 + (int64_t)t * a.Hq;
+  const int t = blockIdx.y, nt = clamp_len(__ldg(a.n + t), a.L);
+  const int x = threadIdx.x % kTokens, y = threadIdx.x / kTokens, p = blockIdx.x * kTokens + x;
+  int s = p < (a.idx ? a.P : nt) ? p : -1;
+  if (a.idx && s >= 0) s = __ldg(a.idx + (int64_t)t * a.P + p);
+  const bool there = s >= 0 && s < nt;
   float w = 0.f;
-#pragma unroll 8
-  for (int h = 0; h < a.Hq; ++h) {
-    const float lz = z[h], x = row[h * a.ldS];
-    w += lz == -INFINITY ? 0.f : exp2_fast(x - lz);
+  if (there) {
+    const float* row = a.logits + (int64_t)t * a.Hq * a.ldS + p;
+    const float* z = a.lse2 + (int64_t)t * a.Hq;
+#pragma unroll (SHARE == 1 ? 8 : 16)
+    for (int h = y; h < a.Hq; h += SHARE) {
+      const float lz = z[h], v = row[h * a.ldS];
+      w += lz == -INFINITY ? 0.f : exp2_fast(v - lz);
+    }
   }
+  if (SHARE > 1) {
+    part[y][x] = w;
+    __syncthreads();
+    if (y != 0) return;
+    w = part[0][x];
+#pragma unroll
+    for (int i = 1; i < SHARE; ++i) w += part[i][x];
+  }
+  if (!there) return;
   float* dst = acc + (int64_t)t * ld + s;
   if (a.idx) atomicAdd(dst, w);
   else *dst += w;
@@ -756,8 +828,21 @@ void launch_attn(const AttnArgs& a, float* acc, int64_t ld_acc, int64_t ctas, cu
     if (a.idx) kv4_attn_kernel<D, NT, SPLIT, true><<<(unsigned)ctas, kThreads, 0, s>>>(a);
     else kv4_attn_kernel<D, NT, SPLIT, false><<<(unsigned)ctas, kThreads, 0, s>>>(a);
   }
-  launch_pdl(kv4_join_kernel<D, SPLIT>, dim3((unsigned)(a.T * a.Hq)), dim3(256), 0, s, a, 8 * NT, ctas);
-  if (acc) launch_pdl(kv4_weights_kernel, dim3((a.P + 255) / 256, a.T), dim3(256), 0, s, a, acc, ld_acc);
+  // A CTA a head where a wave of them is enough (a warp each is slower by 2 us) or where the pieces are many (74 of
+  // them, 16K tokens of one sequence, took a warp 25 us), else a warp: 2048 heads of 5 pieces 6 us for 11.
+  const int heads = a.T * a.Hq;
+  const bool wide = heads <= 148 * 4 || ctas > 16 * (int64_t)(a.T * a.pool.Hkv * a.groups);
+  if (wide) launch_pdl(kv4_join_kernel<D, SPLIT, true>, dim3(heads), dim3(256), 0, s, a, 8 * NT, ctas);
+  else launch_pdl(kv4_join_kernel<D, SPLIT, false>, dim3((heads + 7) / 8), dim3(256), 0, s, a, 8 * NT, ctas);
+  if (acc) {
+    // few positions do not fill the GPU with a thread each: 32 x 2048 selected ones take 9 us for 15 with four;
+    // 32 x 16384 take 10 us, with four 14
+    auto weights = [&](auto kernel, int tokens) {
+      launch_pdl(kernel, dim3((a.P + tokens - 1) / tokens, a.T), dim3(256), 0, s, a, acc, ld_acc);
+    };
+    if ((int64_t)a.T * a.P <= 148 * 1024) weights(kv4_weights_kernel<4>, 64);
+    else weights(kv4_weights_kernel<1>, 256);
+  }
 }
 
 }  // namespace
