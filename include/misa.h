@@ -417,8 +417,8 @@ misa_status misa_evict_select(const float* acc, int64_t ld_acc, const int32_t* n
 
 /*
  * Closes up caches after misa_evict_select, in place: row idx[t][j] of sequence t moves to row j, for
- * the 4-bit cache or the indexer's paged keys (pool [num_pages][page_size][128] of dtype).  idx is
- * ascending with -1 behind the last, as misa_evict_select writes it.  Rows from the number kept on keep
+ * the 4-bit cache or the indexer's paged keys (pool [num_pages][page_size][128] of dtype).  idx ascends
+ * strictly, with -1 behind the last, as misa_evict_select writes it.  Rows from the number kept on keep
  * their contents; block means of the keys are pooled again with misa_pool_keys_paged.  The pages of the
  * T sequences must be theirs alone.
  *   ws : misa_workspace_bytes(MISA_OP_KV4_COMPACT, T, 0, H_kv, 0, d, keep, 0), and
@@ -452,8 +452,9 @@ misa_status misa_prompt_attention(const void* q, const void* k, const void* v, i
 
 /*
  * Device-side status of the calls made so far on the current device.  The tensor-core kernels
- * (scoring and routing queries that share one bf16 cache, and the re-rank of gathered candidates)
- * pipeline their copies and MMAs through shared-memory barriers; every wait on them is bounded
+ * (scoring and routing queries that share one bf16 cache, the re-rank of gathered candidates, and
+ * prompt attention) pipeline their copies and MMAs through shared-memory barriers, and the calls that
+ * close up caches wait for rows to be read before they write over them; every such wait is bounded
  * (about one second).  A wait that runs
  * out makes the kernel stop early, leaving its outputs incomplete, and records the event in a
  * per-device status word.  This call waits for all work on the device to finish
@@ -471,9 +472,9 @@ misa_status misa_device_check(void);
  * it lies outside its range is also counted on the device, by kind:
  *   out[0] routed head ids outside [0, H_I)            (scoring and block-filter calls)
  *   out[1] candidate token ids outside [0, n_t), other than the empty marker -1 (re-rank calls,
- *          paged or not; the header's "empty slot" rule still applies: they are skipped)
+ *          paged or not, and attention over selected tokens; the header's "empty slot" rule still applies: they are skipped)
  *   out[2] page-table entries inside a prefix outside [0, num_pages) (paged calls; per key row
- *          read through the entry)
+ *          read through the entry, in attention over a whole prefix per 16 of them)
  * The counts are occurrences seen, not distinct ids.  In both builds such ids are never
  * dereferenced.  misa_device_check returns MISA_ERR_BAD_INDEX (after MISA_ERR_DEVICE_TIMEOUT,
  * which takes precedence) when any count is nonzero, and clears them.

@@ -825,14 +825,29 @@ _by_handle = {}  # (device index, stream handle) -> the default Workspace of tha
 
 
 def _scratch(ws: Optional["Workspace"], t: torch.Tensor, cur: int, nbytes: int, stream, handle: int):
-    """Pointer of nbytes of the caller's Workspace, or of the stream's default one."""
+    """nbytes of scratch for one call: the caller's Workspace, or the stream's default one, or, for a call
+    that is captured without a Workspace, a buffer of the graph's own (two graphs that were captured on one
+    stream may be replayed on two, and no later call can take the buffer away)."""
+    if nbytes == 0:
+        return None
     if ws is None:
+        if stream is None:
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+        else:
+            with torch.cuda.stream(stream):
+                if torch.cuda.is_current_stream_capturing():
+                    return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
         ws = _by_handle.get((cur, handle))
         if ws is None:
             ws = _by_handle[(cur, handle)] = _ws(None, t.device, stream)
     if ws.buf is None or ws.buf.numel() < nbytes or ws._home != handle:
         ws.get(nbytes, stream)
-    return ws.buf.data_ptr()
+    return ws.buf
+
+
+def _address(buf) -> Optional[int]:
+    return None if buf is None else buf.data_ptr()
 
 
 @functools.lru_cache(maxsize=4096)
@@ -976,11 +991,12 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
         lse = torch.empty((T, H_q), dtype=torch.float32, device=q.device)
     h = _handle(stream, cur)
     nbytes = _ws_bytes(OP_KV4_ATTENTION, T, L, H_q, H_kv, d, P, int(acc is not None))
+    buf = _scratch(ws, q, cur, nbytes, stream, h)
     _check("misa_kv4_attention", _lib.misa_kv4_attention(
         qp, pp, num_pages, page_size, tp, max_pages, np_, ip, T, L, P, H_q, H_kv, d, code,
         d ** -0.5 if scale is None else scale, k_scale, v_scale, _ready(out, "out", q.dtype, cur),
         _ready(lse, "lse", torch.float32, cur), ap, 0 if acc is None else acc.shape[1],
-        _scratch(ws, q, cur, nbytes, stream, h) if nbytes else None, nbytes, h))
+        _address(buf), nbytes, h))
     return out, lse
 
 
@@ -1026,9 +1042,10 @@ def misa_kv4_compact(pool, page_table, idx, d: int, ws: Optional[Workspace] = No
     pp, tp = _ready(pool, "pool", torch.uint8, cur), _ready(page_table, "page_table", torch.int32, cur)
     ip, h = _ready(idx, "idx", torch.int32, cur), _handle(stream, cur)
     nbytes = _ws_bytes(OP_KV4_COMPACT, T, 0, H_kv, 0, d, keep, 0)
+    buf = _scratch(ws, pool, cur, nbytes, stream, h)
     _check("misa_kv4_compact", _lib.misa_kv4_compact(
         pp, num_pages, page_size, tp, max_pages, ip, T, keep, H_kv, d,
-        _scratch(ws, pool, cur, nbytes, stream, h) if nbytes else None, nbytes, h))
+        _address(buf), nbytes, h))
 
 
 def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = None, stream=None) -> None:
@@ -1046,9 +1063,10 @@ def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = Non
     ip, h = _ready(idx, "idx", torch.int32, cur), _handle(stream, cur)
     num_pages, page_size, d = pool.shape
     nbytes = _ws_bytes(OP_KEYS_COMPACT_PAGED, T, 0, 0, 0, d * pool.element_size(), keep, 0)
+    buf = _scratch(ws, pool, cur, nbytes, stream, h)
     _check("misa_keys_compact_paged", _lib.misa_keys_compact_paged(
         pp, num_pages, page_size, tp, page_table.shape[1], ip, T, keep, d, code,
-        _scratch(ws, pool, cur, nbytes, stream, h) if nbytes else None, nbytes, h))
+        _address(buf), nbytes, h))
 
 
 def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, lse=None,
@@ -1080,8 +1098,9 @@ def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = Non
         lse = torch.empty((Tq, H_q), dtype=torch.float32, device=q.device)
     h = _handle(stream, cur)
     nbytes = _ws_bytes(OP_PROMPT_ATTENTION, Tq, Tk, H_q, S, d, 0, 0)
+    buf = _scratch(ws, q, cur, nbytes, stream, h)
     _check("misa_prompt_attention", _lib.misa_prompt_attention(
         qp, kp, vp, ldq, ldk, ldv, cq, ck, S, Tq, Tk, H_q, H_kv, d, BF16, d ** -0.5 if scale is None else scale,
         _ready(out, "out", bf, cur), _ready(lse, "lse", torch.float32, cur),
-        _scratch(ws, q, cur, nbytes, stream, h) if nbytes else None, nbytes, h))
+        _address(buf), nbytes, h))
     return out, lse

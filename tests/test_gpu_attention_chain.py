@@ -105,3 +105,60 @@ def test_prompt_decode_evict_decode():
     for _ in range(2):
         step()
     M.misa_device_check()
+
+
+def test_graphs_captured_without_a_workspace_replay_at_once():
+    """Two graphs of the same calls, captured one after the other on one stream, keep scratch of their own: they
+    are replayed on two streams at once, after an eager call has taken more scratch."""
+    M = lib()
+    T, Hq, Hkv, d, page, cap, keep = 4, 16, 2, 128, 64, 2048, 1500
+    gen = torch.Generator("cuda").manual_seed(5)
+    randn = lambda *s: torch.randn(*s, device="cuda", generator=gen).bfloat16()  # noqa: E731
+    table = torch.arange(T * cap // page, device="cuda", dtype=torch.int32).reshape(T, -1)
+    n = torch.full((T,), cap, device="cuda", dtype=torch.int32)
+    cu = torch.arange(T + 1, device="cuda", dtype=torch.int32) * cap
+    zero = torch.zeros(T, device="cuda", dtype=torch.int32)
+    cq, ck = (torch.tensor([0, x], device="cuda", dtype=torch.int32) for x in (300, 9000))
+    idx = torch.stack([torch.randperm(cap, device="cuda", generator=gen)[:keep].sort().values for _ in range(T)]).int()
+
+    def state():
+        pool = M.misa_kv4_pool(T * cap // page, page, Hkv, d)
+        M.misa_kv4_append(randn(T * cap, Hkv, d), randn(T * cap, Hkv, d), pool, table, cu, zero)
+        return dict(pool=pool, q=randn(T, Hq, d), acc=torch.zeros(T, cap, device="cuda"), pq=randn(300, 4, d),
+                    pk=randn(9000, 2, d), pv=randn(9000, 2, d))
+
+    def run(s):
+        out, lse = M.misa_kv4_attention(s["q"], s["pool"], table, n, acc=s["acc"], want_lse=True)
+        pout, _ = M.misa_prompt_attention(s["pq"], s["pk"], s["pv"], cq, ck)
+        M.misa_kv4_compact(s["pool"], table, idx, d)
+        return out, lse, pout
+
+    states = [state() for _ in range(2)]
+    kept = [{k: s[k].clone() for k in ("pool", "acc")} for s in states]
+    want = [(*run(s), s["pool"].clone(), s["acc"].clone()) for s in states]
+    graphs, outs = [], []
+    side = torch.cuda.Stream()
+    for s in states:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(run(s))
+        graphs.append(g)
+    with torch.cuda.stream(side):  # more scratch than the captured calls took
+        big = randn(8, 64, d)
+        wide = torch.arange(8 * cap // page, device="cuda", dtype=torch.int32).reshape(8, -1) % (T * cap // page)
+        M.misa_kv4_attention(big, states[0]["pool"], wide, torch.full((8,), cap, device="cuda", dtype=torch.int32),
+                             acc=torch.zeros(8, cap, device="cuda"))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for s, k in zip(states, kept):
+            for name in k:
+                s[name].copy_(k[name])
+        torch.cuda.synchronize()
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for s, o, w in zip(states, outs, want):
+            assert all(torch.equal(x, y) for x, y in zip((*o, s["pool"], s["acc"]), w))
+    M.misa_device_check()

@@ -227,6 +227,15 @@ def test_attention_of_more_queries_than_one_launch_takes():
     check_attention(lib(), rng, len(lens), lens, 2, 1, 64, 16, "bf16", acc=True)
 
 
+@pytest.mark.parametrize("pick", [None, 300])
+@pytest.mark.parametrize("d,Hq,Hkv", [(128, 16, 2), (64, 36, 3)])
+def test_many_heads_of_a_few_pieces_each(pick, d, Hq, Hkv):
+    """More heads than one wave of CTAs, cut into pieces by the split of the tokens."""
+    rng = np.random.default_rng(Hq)
+    lens = rng.integers(0, 1500, 38).tolist() + [4096, 0]
+    check_attention(lib(), rng, len(lens), lens, Hq, Hkv, d, 64, "bf16", pick=pick, acc=True)
+
+
 def test_a_token_named_twice_counts_twice():
     M = lib()
     rng = np.random.default_rng(12)
