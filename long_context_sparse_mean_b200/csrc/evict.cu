@@ -23,12 +23,13 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kOneCta = 4096;  // rows up to here take one CTA: a cluster's barriers cost more than they save
+constexpr int kHold = 16;     // tokens a thread holds in registers
 static_assert(kBins == 4 * kThreads, "a thread owns four bins");
 
 // Order of the summed weights; NaN counts as the smallest.
 __device__ __forceinline__ uint32_t weight_key(float f) { return f == f ? order_key(f) : 0u; }
 
-template <int kCluster>
+template <int kCluster, int HOLD>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     evict_select_kernel(const float* __restrict__ acc, int64_t ld, const int32_t* __restrict__ n, int L, int keep,
                         int sink, int recent, int32_t* __restrict__ idx, int32_t* __restrict__ n_out,
@@ -60,19 +61,33 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   uint32_t want = (uint32_t)(keep - sink - recent);  // how many of them stay
   uint32_t cut = 0u;                               // the smallest kept key, of which `want` stay in the end
   const bool choose = want > 0;
+  // runs of consecutive tokens, one a thread; their keys stay in registers where a run is at most HOLD
+  const int run = (nt + kCluster * kThreads - 1) / (kCluster * kThreads);
+  const int r0 = (int)min((int64_t)nt, (int64_t)me * run), r1 = min(nt, r0 + run);
+  float held_w[HOLD > 0 ? HOLD : 1];
+#pragma unroll
+  for (int i = 0; i < HOLD; ++i) held_w[i] = r0 + i < r1 ? __ldg(row + r0 + i) : 0.f;
+  auto each = [&](auto f) {  // of the thread's tokens, in order
+    if (HOLD > 0) {
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i)
+        if (r0 + i < r1) f(r0 + i, held_w[i]);
+    } else {
+#pragma unroll 4
+      for (int s = r0; s < r1; ++s) f(s, __ldg(row + s));
+    }
+  };
+  auto held = [&](int s) { return s < s0 || s >= s1; };
   if (choose) {
     for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) hist[0][i] = 0;
     __syncthreads();
-    const int part = (s1 - s0 + kCluster - 1) / kCluster;
-    const int a = s0 + rank * part, b = min(s1, a + part);
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-#pragma unroll 4
-      for (int s = a + (int)threadIdx.x; s < b; s += kThreads) {
-        const uint32_t k = weight_key(__ldg(row + s));
-        if (pass == 0 || (k >> (shift + bits)) == (cut >> (shift + bits)))
+      each([&](int s, float w) {
+        const uint32_t k = weight_key(w);
+        if (!held(s) && (pass == 0 || (k >> (shift + bits)) == (cut >> (shift + bits))))
           atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1)], 1u);
-      }
+      });
       if (kCluster > 1) cluster.sync();
       else __syncthreads();
       // thread i owns four bins, the largest first
@@ -103,16 +118,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       __syncthreads();
     }
   }
-  // runs of consecutive tokens, one a thread
-  const int run = (nt + kCluster * kThreads - 1) / (kCluster * kThreads);
-  const int r0 = (int)min((int64_t)nt, (int64_t)me * run), r1 = min(nt, r0 + run);
-  auto held = [&](int s) { return s < s0 || s >= s1; };
   uint32_t sure = 0, equal = 0;
-  for (int s = r0; s < r1; ++s) {
-    const uint32_t k = weight_key(__ldg(row + s));
+  each([&](int s, float w) {
+    const uint32_t k = weight_key(w);
     sure += held(s) || (choose && k > cut);
     equal += !held(s) && choose && k == cut;
-  }
+  });
   uint32_t sure_all, equal_all;
   uint32_t sure_at = block_exclusive_scan(sure, warp_tot, &sure_all);
   uint32_t equal_at = block_exclusive_scan(equal, warp_tot, &equal_all);
@@ -126,8 +137,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     sure_at += c[0];
     equal_at += c[1];
   }
-  for (int s = r0; s < r1; ++s) {
-    const float v = __ldg(row + s);
+  each([&](int s, float v) {
     const uint32_t k = weight_key(v);
     const bool eq = !held(s) && choose && k == cut;
     const bool stay = held(s) || (choose && k > cut) || (eq && equal_at < want);
@@ -139,7 +149,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     }
     sure_at += stay && !eq;
     equal_at += eq;
-  }
+  });
   if (kCluster > 1) cluster.sync();  // no CTA leaves while another may read its counts
 }
 
@@ -151,8 +161,9 @@ void launch_evict_select(const float* acc, int64_t ld, const int32_t* n, int T, 
   auto run = [&](auto kernel, int cluster) {
     kernel<<<T * cluster, kThreads, 0, s>>>(acc, ld, n, L, keep, sink, recent, idx, n_out, acc_out, ld_out);
   };
-  if (L <= kOneCta) run(evict_select_kernel<1>, 1);
-  else run(evict_select_kernel<8>, 8);
+  if (L <= kOneCta) run(evict_select_kernel<1, kOneCta / kThreads>, 1);
+  else if (L <= 8 * kThreads * kHold) run(evict_select_kernel<8, kHold>, 8);
+  else run(evict_select_kernel<8, 0>, 8);
 }
 
 }  // namespace misa
