@@ -2,14 +2,15 @@
 // gathered: the first `sink`, the last `recent`, and of those between the ones with the largest summed
 // weight (ties to the lower token).
 //
-// A row is read a handful of times, from the L2 after the first, and little is written, so a call lasts
-// as long as its chain of dependent steps; the work of a row is spread over a cluster of 8 CTAs to keep
-// each step short.  Three histogram passes over the row's order keys (11, 11 and 10 bits) find the last
-// kept key and how many of its equals stay: each CTA counts its eighth of the row in shared memory, and
-// all add up the eight histograms through distributed shared memory.  Then every thread counts the kept
-// tokens of its own run of consecutive tokens, one scan over the CTA and the counts of the CTAs before it
-// say where they go, and they are written in order.  (One CTA a row, with a scan for every 1024 tokens:
-// 55.7 us for 16 rows of up to 32768 tokens.)
+// Little is read and written, so a call lasts as long as its chain of dependent steps; the work of a row is
+// spread over a cluster of 8 CTAs to keep each step short, and its weights stay in registers, a run of
+// consecutive tokens a thread, where the runs are short enough.  Three histogram passes over the order keys
+// (11, 11 and 10 bits) find the last kept key and how many of its equals stay: each CTA counts its tokens in
+// shared memory, and all add up the eight histograms through distributed shared memory.  Then every thread
+// counts the kept tokens of its run, one scan over the CTA and the counts of the CTAs before it say where they
+// go, and they are written in order.
+// 16 rows of up to 32768 tokens: 18.5 us (one CTA a row, with a scan for every 1024 tokens: 55.7; read in every
+// pass: 22); one row of 1000 tokens: 6.4 us.
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"
@@ -23,7 +24,6 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kOneCta = 4096;  // rows up to here take one CTA: a cluster's barriers cost more than they save
-constexpr int kHold = 16;     // tokens a thread holds in registers
 static_assert(kBins == 4 * kThreads, "a thread owns four bins");
 
 // Order of the summed weights; NaN counts as the smallest.
@@ -83,11 +83,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     __syncthreads();
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      each([&](int s, float w) {
+      auto count = [&](int s, float w) {
         const uint32_t k = weight_key(w);
         if (!held(s) && (pass == 0 || (k >> (shift + bits)) == (cut >> (shift + bits))))
           atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1)], 1u);
-      });
+      };
+      if (HOLD > 0) {
+        each(count);
+      } else {  // in any order: neighbours by neighbouring threads
+#pragma unroll 8
+        for (int s = s0 + me; s < s1; s += kCluster * kThreads) count(s, __ldg(row + s));
+      }
       if (kCluster > 1) cluster.sync();
       else __syncthreads();
       // thread i owns four bins, the largest first
@@ -162,7 +168,11 @@ void launch_evict_select(const float* acc, int64_t ld, const int32_t* n, int T, 
     kernel<<<T * cluster, kThreads, 0, s>>>(acc, ld, n, L, keep, sink, recent, idx, n_out, acc_out, ld_out);
   };
   if (L <= kOneCta) run(evict_select_kernel<1, kOneCta / kThreads>, 1);
-  else if (L <= 8 * kThreads * kHold) run(evict_select_kernel<8, kHold>, 8);
+  // registers for as long a run as the longest row has, up to 32 (one row of 128K tokens with both compactions:
+  // 115 us, 129 us when it is read in every pass)
+  else if (L <= 8 * 8 * kThreads) run(evict_select_kernel<8, 8>, 8);
+  else if (L <= 8 * 16 * kThreads) run(evict_select_kernel<8, 16>, 8);
+  else if (L <= 8 * 32 * kThreads) run(evict_select_kernel<8, 32>, 8);
   else run(evict_select_kernel<8, 0>, 8);
 }
 

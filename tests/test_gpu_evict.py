@@ -56,6 +56,19 @@ def test_the_tokens_that_stay(kind, lens, keep, sink, recent):
         assert np.all(host(ao)[t, len(want):] == 0)
 
 
+@pytest.mark.parametrize("kind", ["plain", "odd", "equal"])
+@pytest.mark.parametrize("lens,keep", [([40000, 32769], 17000), ([131072, 3, 65537], 2000), ([140000, 139999], 70000)])
+def test_long_rows(kind, lens, keep):
+    M = lib()
+    rng = np.random.default_rng(keep)
+    acc = weights(rng, len(lens), max(lens), kind)
+    idx, no, ao = M.misa_evict_select(cuda(acc), cuda(np.array(lens, np.int32)), keep, 4, 33, want_acc=True)
+    for t in range(len(lens)):
+        want = R.evict(acc[t], lens[t], keep, 4, 33)
+        assert int(no[t]) == len(want) and host(idx)[t].tolist() == want + [-1] * (keep - len(want))
+        assert np.array_equal(host(ao)[t, :len(want)], acc[t, want], equal_nan=True)
+
+
 def test_lengths_outside_the_row_and_limits():
     M = lib()
     acc = np.random.default_rng(1).random((3, 50)).astype(np.float32)
