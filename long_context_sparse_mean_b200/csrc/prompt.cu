@@ -33,8 +33,8 @@
 // before, in fp32.  Values that are not finite and were set to zero are added to the rows that do see
 // them at the end.
 //
-// Which CTA does what: with many items one CTA takes one item, and the GPU's own dispatch evens them out;
-// with few, or few long ones, 148 CTAs share the items' blocks equally, an item that a boundary cuts is
+// Which CTA does what: with many long items one CTA takes one item, and the GPU's own dispatch evens them out;
+// with short ones, or few long ones, 148 CTAs share the items' blocks equally, an item that a boundary cuts is
 // left in pieces, and a last kernel joins them (130 queries over 20000 keys keep every SM busy).
 // Every wait is bounded in time; a wait that runs out sets a device status word and all roles leave
 // their loops, wait for their own copies and MMAs, and free tensor memory.
@@ -235,6 +235,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Warp-wide: lane l reads 16 consecutive columns of TMEM lane (taddr.lane + l); the values are there on return.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// 32 bytes, a whole sector, in one store; p is 32-byte aligned.
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                : "memory");
 }
 
@@ -646,28 +665,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = 2 * blockIdx.x + (walk.j0 == 0 ? 1 : 0);
         __nv_bfloat16* out = a.out + ((int64_t)(p.row + i) * a.Hq + walk.head) * D;
         float* part = a.plan.part + (int64_t)slot * D * kPair + i;
-        // eight outputs at a time, in a loop of few instructions: once an item, this code is not in the
+        // a row's outputs go out by whole sectors of 32 bytes (packed prompts of 200 to 4096 tokens: 473 us, 491 by
+        // halves of them)
+        const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
+        // sixteen outputs at a time, in a loop of few instructions: once an item, this code is not in the
         // instruction cache when it runs
 #pragma unroll 1
-        for (int x = 0; x < D; x += 8) {
-          uint32_t o[8];
+        for (int x = 0; x < D; x += 16) {
+          uint32_t o[16];
           if (to_ > from) {
-            tmem_ld8(to + x, o);
+            tmem_ld16(to + x, o);
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = 0u;
+            for (int e = 0; e < 16; ++e) o[e] = 0u;
           }
           if (!whole) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) part[(x + e) * kPair] = __uint_as_float(o[e]);
+            for (int e = 0; e < 16; ++e) part[(x + e) * kPair] = __uint_as_float(o[e]);
           } else {
-            uint32_t w[4];
+            uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 8; ++e) {
               const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
               w[e] = *reinterpret_cast<const uint32_t*>(&h);
             }
-            if (i < p.rows) *reinterpret_cast<uint4*>(out + x) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (i < p.rows) {
+              if (sectors) {
+                store32(out + x, w);
+              } else {
+                reinterpret_cast<uint4*>(out + x)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(out + x)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
           }
         }
         if (to_ > from) {  // the next segment may overwrite O
@@ -975,10 +1004,13 @@ int64_t most_pairs(int S, int Tq) { return (int64_t)Tq / kPair + std::min(S, Tq)
 
 // Whether a call goes without a plan, one item a CTA: where the items are few enough for one CTA an SM and
 // none is long (32 blocks of keys at most), so that cutting them up would not pay for the two launches it
-// adds, and where they are many, so that the GPU's own dispatch evens them out.
+// adds, and where they are many and take long enough (more than 8 blocks of keys a sequence) for the GPU's own
+// dispatch to even them out.  (Short ones gain from CTAs that stay: their loads and first scores go ahead of
+// the last item's end.  32 heads, sequences of 256 tokens: 218 us for 317; of 1024: 407 for 417; of 2048: 549
+// for 540; of 4096: 867 for 820.)
 bool plain_call(int S, int Tq, int Tk, int Hq) {
   const int64_t items = most_pairs(S, Tq) * Hq;
-  return items > kManyItems || (items <= kCtas && Tk <= 32 * kRows);
+  return (items > kManyItems && Tk > 8 * kRows * (int64_t)S) || (items <= kCtas && Tk <= 32 * kRows);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }

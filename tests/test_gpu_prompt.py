@@ -97,6 +97,22 @@ def test_items_cut_between_ctas(d, Hq, Hkv, lens, extra):
     M.misa_device_check()
 
 
+def test_many_long_items_and_an_output_between_sectors():
+    M = lib()
+    rng = np.random.default_rng(31)
+    lens, extra, Hq, Hkv, d = [1100, 1500, 0, 1300, 1, 900], [0, 0, 0, 1000, 4000, 300], 40, 8, 64
+    cu_q, cu_k = cum(lens), cum([a + b for a, b in zip(lens, extra)])
+    q = cuda(rng.standard_normal((cu_q[-1], Hq, d)).astype(np.float32) * 2, torch.bfloat16)
+    k, v = (cuda(rng.standard_normal((cu_k[-1], Hkv, d)).astype(np.float32), torch.bfloat16) for _ in range(2))
+    out, lse = M.misa_prompt_attention(q, k, v, cuda(cu_q), cuda(cu_k), want_lse=True)
+    check(M, q, k, v, cu_q, cu_k, out, lse, d ** -0.5, rows=12)
+    room = torch.full((q.numel() + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    other = room[8:8 + q.numel()].view_as(q)  # 16 bytes past a 256-byte boundary
+    M.misa_prompt_attention(q, k, v, cuda(cu_q), cuda(cu_k), out=other)
+    assert torch.equal(other, out) and (room[:8] == 7).all() and (room[-8:] == 7).all()
+    M.misa_device_check()
+
+
 def test_sharp_and_flat_logits_and_growing_maxima():
     M = lib()
     rng = np.random.default_rng(5)
