@@ -278,7 +278,8 @@ __device__ __forceinline__ int4 sequence(const PromptArgs& a, int b) {
 
 // Without a plan: the pair of CTA x / Hq, pairs of every sequence from its last to its first.  False when
 // there is none.  Every thread of the block calls it.
-__device__ __forceinline__ bool find_pair(const PromptArgs& a, int pair, Pair& p, uint32_t* warp_tot, Pair* found, int* hit) {
+__device__ __forceinline__ bool find_pair(const PromptArgs& a, int pair, Pair& p, uint32_t* warp_tot, Pair* found,
+                                          int* hit) {
   int base = 0;
   if (threadIdx.x == 0) *hit = 0;
   for (int b0 = 0; b0 < a.S; b0 += kThreads) {
@@ -334,7 +335,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(const PromptA
   for (int p0 = 0; p0 < n; p0 += kPlanThreads) {
     const int p = p0 + (int)threadIdx.x;
     uint32_t total;
-    const uint32_t before = block_exclusive_scan(p < n ? (uint32_t)(a.plan.pairs[p].count + kItemCost) : 0u, warp_tot, &total);
+    const uint32_t cost = p < n ? (uint32_t)(a.plan.pairs[p].count + kItemCost) : 0u;
+    const uint32_t before = block_exclusive_scan(cost, warp_tot, &total);
     if (p < n) {
       const uint64_t v = carry + before;
       a.plan.cost[p] = v;
@@ -578,8 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         float neg = m == -INFINITY ? 0.f : -m * c;
         sum[0] = sum[1] = make_float2(0.f, 0.f);
         auto start = [&](int e) {  // exponentials of pair e
-          const float2 z = __ffma2_rn(make_float2(__uint_as_float(s[e / 16][2 * (e % 16)]), __uint_as_float(s[e / 16][2 * (e % 16) + 1])),
-                                      make_float2(c, c), make_float2(neg, neg));
+          const uint32_t(&x)[32] = s[e / 16];
+          const float2 y = make_float2(__uint_as_float(x[2 * (e % 16)]), __uint_as_float(x[2 * (e % 16) + 1]));
+          const float2 z = __ffma2_rn(y, make_float2(c, c), make_float2(neg, neg));
           w[e % kLag] = make_float2(ex2(z.x), ex2(z.y));
         };
         auto finish = [&](int e) {  // its sum and its rounding
@@ -597,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (e < 16) {
             start(e);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) top[x] = max3(top[x], __uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1]));
+            for (int x = 0; x < 4; ++x)
+              top[x] = max3(top[x], __uint_as_float(s[x][2 * e]), __uint_as_float(s[x][2 * e + 1]));
           }
         }
         const float mx = max3(fmaxf(top[0], top[1]), top[2], top[3]);
@@ -686,7 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+              const __nv_bfloat162 h =
+                  __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
               w[e] = *reinterpret_cast<const uint32_t*>(&h);
             }
             if (i < p.rows) {
@@ -708,7 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.plan.part_ml[(slot * 2) * kPair + i] = m;
           a.plan.part_ml[(slot * 2 + 1) * kPair + i] = l;
         } else if (a.lse && i < p.rows) {
-          a.lse[((int64_t)p.row + i) * a.Hq + walk.head] = l == 0.f ? -INFINITY : m * c * 0.693147180559945309f + logf(l);
+          a.lse[((int64_t)p.row + i) * a.Hq + walk.head] =
+              l == 0.f ? -INFINITY : m * c * 0.693147180559945309f + logf(l);
         }
         if (odd[seg & 3] == seg + 1 && i < p.rows)
           add_strange<D>(a.v + (int64_t)p.key0 * a.ldv + (walk.head / a.G) * D, a.ldv, p, from, to_, i,
@@ -800,7 +806,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++qn;
           }
           if (!wait(full(b), (u / NB) & 1)) return;
-          const uint64_t qd = tc::sw128_kmajor_desc(qbase + t * L::kTileBytes), kd = tc::sw128_kmajor_desc(ring + b * L::kTileBytes);
+          const uint64_t qd = tc::sw128_kmajor_desc(qbase + t * L::kTileBytes);
+          const uint64_t kd = tc::sw128_kmajor_desc(ring + b * L::kTileBytes);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t at = ((kk / 4) * L::kHalfBytes + (kk % 4) * 32) >> 4;
@@ -886,7 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          if (!walk.guarded(j)) {  // passed on all the same: a guard that fell behind by a turn of the ring would miss its phase
+          // passed on all the same: a guard that fell behind by a turn of the ring would miss its phase
+          if (!walk.guarded(j)) {
             if (lane == 0) tc::mbar_arrive(vok(b));
             continue;
           }
