@@ -31,12 +31,19 @@ __device__ __forceinline__ float divide(float x, float b, float y) {
   return fmaf(fmaf(-q, b, x), y, q);
 }
 
+// The larger one; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Both kernels: four threads a row of a head and side; thread c has the elements 16 j + 4 c .. + 3 of every
 // block j, which are chunk c of the code row, so codes move in whole 16-byte (d = 64: 8-byte) words and
 // the elements in 8- or 16-byte pieces of which four threads cover a full 32- or 64-byte stretch.  What
 // bounds them is HBM: every element is read or written once in its own type, every code once.  13.3K rows of 8
-// heads of 128 in bf16: append 31 us, 2.2 TB/s (most of it conversions: a division and two roundings an element),
-// read back 15 us, 4.6 TB/s.
+// heads of 128 in bf16: append 24.6 us, 2.8 TB/s (conversions and the five operations of a
+// quotient for every element; with the scales worked out by all four threads 31.3), read back 15.2 us, 4.6 TB/s.
 template <int D, DType DT>
 __global__ void __launch_bounds__(256) kv4_append_kernel(const void* __restrict__ k, const void* __restrict__ v,
                                                          int64_t ldk, int64_t ldv, Kv4Pool pool,
@@ -46,9 +53,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const void* __restrict_
   constexpr int NB = D / 16;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int c = (int)(i & 3), sides = 2 * pool.Hkv;
-  const int64_t u = i >> 2, r = u / sides;
-  const bool in = r < rows;  // whole groups of four threads alike; they exchange maxima below
-  const int sl = (int)(u - r * sides), h = sl >> 1, side = sl & 1;
+  const bool in = (i >> 2) < (int64_t)rows * sides;  // whole groups of four threads alike; they exchange maxima below
+  const uint32_t u = (uint32_t)(i >> 2);             // rows and heads are bounded: 32 bits hold it
+  const int64_t r = u / (uint32_t)sides;
+  const int sl = (int)(u - (uint32_t)r * sides), h = sl >> 1, side = sl & 1;
   float x[NB][4];
   if (in) {
     const int64_t at = r * (side ? ldv : ldk) + (int64_t)h * D + 4 * c;
@@ -79,26 +87,63 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const void* __restrict_
     s = (int64_t)__ldg(start + seq) + (r - __ldg(cu + seq));
     pg = kv4_page(pool, seq, s, sl == 0 && c == 0);
   }
+  // The four threads find the largest elements of their NB blocks together, each ending up with those of its own
+  // NB / 4 blocks, whose scales and inverses it works out for all four (a division and a reciprocal to nearest
+  // are as long as all the rest of a block).
+  constexpr int OWN = NB / 4;
   const float g = side ? vg : kg, g6 = g * 6.0f;
+  float top[OWN];
+  auto tops = [&] {
+    float m[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      m[j] = max_nan(max_nan(fabsf(x[j][0]), fabsf(x[j][1])), max_nan(fabsf(x[j][2]), fabsf(x[j][3])));
+#pragma unroll
+    for (int j = 0; j < NB / 2; ++j) {
+      const float got = __shfl_xor_sync(0xffffffffu, c & 2 ? m[j] : m[j + NB / 2], 2);
+      m[j] = max_nan(c & 2 ? m[j + NB / 2] : m[j], got);
+    }
+#pragma unroll
+    for (int j = 0; j < OWN; ++j) {
+      const float got = __shfl_xor_sync(0xffffffffu, c & 1 ? m[j] : m[j + OWN], 1);
+      top[j] = max_nan(c & 1 ? m[j + OWN] : m[j], got);
+    }
+  };
+  tops();
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < OWN; ++j) nan |= top[j] != top[j];
+  if (__any_sync(0xffffffffu, nan)) {  // NaN stores as 0
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[j][e] = x[j][e] == x[j][e] ? x[j][e] : 0.f;
+    tops();
+  }
+  float unit[OWN], inv[OWN];
+  uint32_t s8 = 0;
+#pragma unroll
+  for (int j = 0; j < OWN; ++j) {
+    const uint32_t e = float_to_e4m3(top[j] / g6);
+    unit[j] = e4m3_to_float(e) * g;
+    inv[j] = unit[j] == 0.f ? 0.f : __frcp_rn(unit[j]);  // with both 0 every quotient is 0, of x's sign
+    s8 |= e << (8 * j);
+  }
   uint32_t code[NB / 2], scale[NB / 4];
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    float top = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[j][e] = x[j][e] == x[j][e] ? x[j][e] : 0.f;  // NaN stores as 0
-      top = fmaxf(top, fabsf(x[j][e]));
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const uint32_t s8 = float_to_e4m3(top / g6);
-    const float unit = e4m3_to_float(s8) * g, y = unit == 0.f ? 0.f : __frcp_rn(unit);
-    // with unit 0, y is 0 too, and every quotient is x 0 0 = 0
-    const float z = unit == 0.f ? 0.f : 1.f;
-    const uint32_t w = float2_to_e2m1x2(divide(x[j][0] * z, unit, y), divide(x[j][1] * z, unit, y)) |
-                       (float2_to_e2m1x2(divide(x[j][2] * z, unit, y), divide(x[j][3] * z, unit, y)) << 8);
+    const float u = __shfl_sync(0xffffffffu, unit[j % OWN], j / OWN, 4);
+    const float y = __shfl_sync(0xffffffffu, inv[j % OWN], j / OWN, 4);
+    const uint32_t w = float2_to_e2m1x2(divide(x[j][0], u, y), divide(x[j][1], u, y)) |
+                       (float2_to_e2m1x2(divide(x[j][2], u, y), divide(x[j][3], u, y)) << 8);
     code[j / 2] = j & 1 ? code[j / 2] | (w << 16) : w;
-    scale[j / 4] = j & 3 ? scale[j / 4] | (s8 << (8 * (j & 3))) : s8;
+  }
+#pragma unroll
+  for (int j = 0; j < NB / 4; ++j) {
+    scale[j] = 0;
+#pragma unroll
+    for (int k = 0; k < 4 / OWN; ++k)
+      scale[j] |= __shfl_sync(0xffffffffu, s8, j * (4 / OWN) + k, 4) << (8 * OWN * k);
   }
   if (pg < 0) return;
   uint8_t* slab = pool.base + pg * pool.page_bytes() + (int64_t)sl * pool.slab_bytes();
@@ -121,9 +166,10 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Pool pool, const int32
   constexpr int NB = D / 16;
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int c = (int)(i & 3), sides = 2 * pool.Hkv;
-  const int64_t u = i >> 2, r = u / sides;
-  if (r >= rows) return;
-  const int sl = (int)(u - r * sides), h = sl >> 1, side = sl & 1;
+  if ((i >> 2) >= (int64_t)rows * sides) return;
+  const uint32_t u = (uint32_t)(i >> 2);
+  const int64_t r = u / (uint32_t)sides;
+  const int sl = (int)(u - (uint32_t)r * sides), h = sl >> 1, side = sl & 1;
   const int seq = packed_seq(cu, S, (int)r);
   if (seq < 0) return;
   const int64_t s = (int64_t)__ldg(start + seq) + (r - __ldg(cu + seq));
