@@ -26,12 +26,12 @@
 // where a piece ends inside a head's tokens.  Weights to be summed need the finished log-sums: the logits are
 // kept, and a third kernel turns them into weights.
 //
-// Measured: 16 queries of 64 heads over 120K to 128K tokens on 8 kv heads of d = 128 take 467 us, 4.9 TB/s of
-// cache (0.76 of the measured copy rate; 0.64 instructions a clock and scheduler: without the copies 393 us, without
-// the widening of K 465, of V 428, without the products 469).  Slower: five CTAs an SM at 96 registers 495, K
+// Measured: 16 queries of 64 heads over 120K to 128K tokens on 8 kv heads of d = 128 take 463 us, 5.0 TB/s of
+// cache (0.77 of the measured copy rate; 0.64 instructions a clock and scheduler: of 467 us, 393 without the copies,
+// 465 without the widening of K, 428 of V, 469 without the products).  Slower: five CTAs an SM at 96 registers 495, K
 // and V refilled by themselves 494, bulk copies of 128 bytes to 1 KB 561, of whole pages shared by two warps
-// 526.  32 queries of 32 heads over up to 16K tokens: 46 us, joins 8 and weights 10 us; 2048 selected tokens
-// of 32 queries (64 heads): 48 us for 75 MB in rows of 64 and 8 bytes from anywhere, joins 6, weights 9.
+// 526.  32 queries of 32 heads over up to 16K tokens: 41 us, joins 8 and weights 10 us; 2048 selected tokens
+// of 32 queries (64 heads): 50 us for 75 MB in rows of 64 and 8 bytes from anywhere, joins 6, weights 9.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -47,6 +47,9 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 16;               // tokens of a product's 16 rows; pages hold whole pieces of 16
 constexpr int kTile = 2 * kSub;        // tokens of a warp's step
 constexpr int kUnit = kWarps * kTile;  // tokens of a CTA's step: the grain of the split
+// Units that an item's start and end take as long as, for the even split: without them the CTAs that go from one
+// item to the next end last (64 queries of up to 16K tokens: 112 us, with one 104, two 102, four 104).
+constexpr uint32_t kItemCost = 2;
 constexpr int kMaxT = 256;             // queries per launch
 constexpr int kMaxCtas = 1024;         // bound on the grid, for workspace sizes that ask no device
 // Weights are kept scaled by 2^kLift against the running maximum, which may lag the true one by
@@ -130,7 +133,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Units (of kUnit positions) of every query and their running sum: pre[0 .. T].
+// Units (of kUnit positions) of every query, kItemCost more for every item, and their running sum: pre[0 .. T].
 __device__ __forceinline__ void unit_prefix(const AttnArgs& a, uint64_t* pre, uint64_t* tot) {
   const int per = (a.T + kThreads - 1) / kThreads;
   const int b0 = min(a.T, (int)threadIdx.x * per), b1 = min(a.T, b0 + per);
@@ -139,7 +142,7 @@ __device__ __forceinline__ void unit_prefix(const AttnArgs& a, uint64_t* pre, ui
   for (int t = b0; t < b1; ++t) {
     const int nt = clamp_len(__ldg(a.n + t), a.L);
     const int len = a.idx ? (nt > 0 ? a.P : 0) : nt;
-    local += (uint64_t)((len + kUnit - 1) / kUnit) * (a.pool.Hkv * a.groups);
+    if (len > 0) local += (uint64_t)((len + kUnit - 1) / kUnit + kItemCost) * (a.pool.Hkv * a.groups);
     pre[t + 1] = local;
   }
   uint64_t x = local;
@@ -198,12 +201,14 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(8 * NT)) kv4_attn_kern
   }
   while (pos < end) {
     while (pre[t + 1] <= pos) ++t;
-    const uint32_t units = (uint32_t)((pre[t + 1] - pre[t]) / items);  // of one item
+    const uint32_t span = (uint32_t)((pre[t + 1] - pre[t]) / items), units = span - kItemCost;  // of one item
     const uint64_t at = pos - pre[t];
-    const int item = (int)(at / units);
-    const uint32_t u0 = (uint32_t)(at - (uint64_t)item * units);
-    const uint32_t u1 = (uint32_t)min((uint64_t)units, u0 + (end - pos));
-    pos += u1 - u0;
+    const int item = (int)(at / span);
+    const uint32_t s0 = (uint32_t)(at - (uint64_t)item * span);
+    const uint32_t s1 = (uint32_t)min((uint64_t)span, s0 + (end - pos));
+    pos += s1 - s0;
+    if (s1 <= kItemCost) continue;  // nothing but the item's start
+    const uint32_t u0 = s0 > kItemCost ? s0 - kItemCost : 0u, u1 = s1 - kItemCost;
     const int hk = item / a.groups, hg = item - hk * a.groups;
     const int nt = clamp_len(__ldg(a.n + t), a.L);
     const int len = GATHER ? a.P : nt;
@@ -647,11 +652,11 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, int t, int hq, in
   const int hk = hq / a.G, hr = hq % a.G;
   const int items = a.pool.Hkv * a.groups, item = hk * a.groups + hr / HB;
   const uint64_t W = a.pre[a.T], first = a.pre[t];
-  const uint64_t units = (a.pre[t + 1] - first) / items;
+  const uint64_t span = (a.pre[t + 1] - first) / items;
   Pieces r = {0, 0};
-  if (units > 0) {
+  if (span > 0) {
     const uint64_t grid = W < (uint64_t)ctas ? W : (uint64_t)ctas;
-    const uint64_t p0 = first + item * units, p1 = p0 + units;
+    const uint64_t p0 = first + item * span + kItemCost, p1 = first + (item + 1) * span;
     const int64_t c0 = (int64_t)(((p0 + 1) * grid - 1) / W), c1 = (int64_t)((p1 * grid - 1) / W);
     r.first = c0 + (int64_t)t * items + item;
     r.count = (int)(c1 - c0 + 1);
@@ -824,7 +829,7 @@ int heads_per_item(int G) { return G > 8 ? 16 : 8; }
 
 int64_t attn_ctas(int T, int P, int Hkv, int G) {
   const int HB = heads_per_item(G);
-  const int64_t most = (int64_t)T * Hkv * ((G + HB - 1) / HB) * ((P + kUnit - 1) / kUnit);
+  const int64_t most = (int64_t)T * Hkv * ((G + HB - 1) / HB) * ((P + kUnit - 1) / kUnit + kItemCost);
   const int64_t full = std::min<int64_t>((int64_t)sm_count() * resident_ctas(HB), kMaxCtas);
   return std::min(most, full);
 }
