@@ -48,8 +48,9 @@ constexpr int kSub = 16;               // tokens of a product's 16 rows; pages h
 constexpr int kTile = 2 * kSub;        // tokens of a warp's step
 constexpr int kUnit = kWarps * kTile;  // tokens of a CTA's step: the grain of the split
 // Units that an item's start and end take as long as, for the even split: without them the CTAs that go from one
-// item to the next end last (64 queries of up to 16K tokens: 112 us, with one 104, two 102, four 104).
-constexpr uint32_t kItemCost = 2;
+// item to the next end last (64 queries of up to 16K tokens: 112 us, with one 104, two 102, four 104).  Units of
+// selected tokens take longer, and each CTA few of them (2048 of 32 queries: 63 us without, 69 with two).
+__host__ __device__ constexpr uint32_t item_cost(bool selected) { return selected ? 0u : 2u; }
 constexpr int kMaxT = 256;             // queries per launch
 constexpr int kMaxCtas = 1024;         // bound on the grid, for workspace sizes that ask no device
 // Weights are kept scaled by 2^kLift against the running maximum, which may lag the true one by
@@ -133,7 +134,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Units (of kUnit positions) of every query, kItemCost more for every item, and their running sum: pre[0 .. T].
+// Units (of kUnit positions) of every query, item_cost more for every item, and their running sum: pre[0 .. T].
+template <bool GATHER>
 __device__ __forceinline__ void unit_prefix(const AttnArgs& a, uint64_t* pre, uint64_t* tot) {
   const int per = (a.T + kThreads - 1) / kThreads;
   const int b0 = min(a.T, (int)threadIdx.x * per), b1 = min(a.T, b0 + per);
@@ -142,7 +144,7 @@ __device__ __forceinline__ void unit_prefix(const AttnArgs& a, uint64_t* pre, ui
   for (int t = b0; t < b1; ++t) {
     const int nt = clamp_len(__ldg(a.n + t), a.L);
     const int len = a.idx ? (nt > 0 ? a.P : 0) : nt;
-    if (len > 0) local += (uint64_t)((len + kUnit - 1) / kUnit + kItemCost) * (a.pool.Hkv * a.groups);
+    if (len > 0) local += (uint64_t)((len + kUnit - 1) / kUnit + item_cost(GATHER)) * (a.pool.Hkv * a.groups);
     pre[t + 1] = local;
   }
   uint64_t x = local;
@@ -170,6 +172,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(8 * NT)) kv4_attn_kern
   constexpr int KS = D / 16;      // k-steps of S, and 16-row pieces of O
   constexpr int RB = D / 2;       // bytes of a code row
   constexpr int HB = 8 * NT;      // heads of an item
+  constexpr uint32_t kCost = item_cost(GATHER);
   constexpr int kRing = kWarps * 2 * St::kBytes;
   constexpr int kJoin = kWarps * HB * (D + 2) * 4;
   __shared__ __align__(16) uint8_t ring[kRing > kJoin ? kRing : kJoin];
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(8 * NT)) kv4_attn_kern
   __shared__ uint64_t tot[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   pdl_trigger();
-  unit_prefix(a, pre, tot);
+  unit_prefix<GATHER>(a, pre, tot);
   if (blockIdx.x == 0)
     for (int t = threadIdx.x; t <= a.T; t += kThreads) a.pre[t] = pre[t];
   const uint64_t W = pre[a.T];
@@ -201,14 +204,14 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(8 * NT)) kv4_attn_kern
   }
   while (pos < end) {
     while (pre[t + 1] <= pos) ++t;
-    const uint32_t span = (uint32_t)((pre[t + 1] - pre[t]) / items), units = span - kItemCost;  // of one item
+    const uint32_t span = (uint32_t)((pre[t + 1] - pre[t]) / items), units = span - kCost;  // of one item
     const uint64_t at = pos - pre[t];
     const int item = (int)(at / span);
     const uint32_t s0 = (uint32_t)(at - (uint64_t)item * span);
     const uint32_t s1 = (uint32_t)min((uint64_t)span, s0 + (end - pos));
     pos += s1 - s0;
-    if (s1 <= kItemCost) continue;  // nothing but the item's start
-    const uint32_t u0 = s0 > kItemCost ? s0 - kItemCost : 0u, u1 = s1 - kItemCost;
+    if (s1 <= kCost) continue;  // nothing but the item's start
+    const uint32_t u0 = s0 > kCost ? s0 - kCost : 0u, u1 = s1 - kCost;
     const int hk = item / a.groups, hg = item - hk * a.groups;
     const int nt = clamp_len(__ldg(a.n + t), a.L);
     const int len = GATHER ? a.P : nt;
@@ -656,7 +659,7 @@ __device__ __forceinline__ Pieces pieces_of(const AttnArgs& a, int t, int hq, in
   Pieces r = {0, 0};
   if (span > 0) {
     const uint64_t grid = W < (uint64_t)ctas ? W : (uint64_t)ctas;
-    const uint64_t p0 = first + item * span + kItemCost, p1 = first + (item + 1) * span;
+    const uint64_t p0 = first + item * span + item_cost(a.idx != nullptr), p1 = first + (item + 1) * span;
     const int64_t c0 = (int64_t)(((p0 + 1) * grid - 1) / W), c1 = (int64_t)((p1 * grid - 1) / W);
     r.first = c0 + (int64_t)t * items + item;
     r.count = (int)(c1 - c0 + 1);
@@ -827,9 +830,9 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const AttnArgs a, floa
 
 int heads_per_item(int G) { return G > 8 ? 16 : 8; }
 
-int64_t attn_ctas(int T, int P, int Hkv, int G) {
+int64_t attn_ctas(int T, int P, int Hkv, int G, bool selected) {
   const int HB = heads_per_item(G);
-  const int64_t most = (int64_t)T * Hkv * ((G + HB - 1) / HB) * ((P + kUnit - 1) / kUnit + kItemCost);
+  const int64_t most = (int64_t)T * Hkv * ((G + HB - 1) / HB) * ((P + kUnit - 1) / kUnit + item_cost(selected));
   const int64_t full = std::min<int64_t>((int64_t)sm_count() * resident_ctas(HB), kMaxCtas);
   return std::min(most, full);
 }
@@ -898,7 +901,7 @@ void launch_kv4_attention(DType dt, const void* q, const Kv4Pool& pool, const in
     a.page_mul = pieces == 1 ? 0u : (uint32_t)(((1ull << 32) + pieces - 1) / pieces);
     a.out = static_cast<char*>(out) + elt * t0 * (size_t)Hq * pool.d;
     a.lse = lse ? lse + (int64_t)t0 * Hq : nullptr;
-    const int64_t ctas = attn_ctas(Tc, a.P, pool.Hkv, G);
+    const int64_t ctas = attn_ctas(Tc, a.P, pool.Hkv, G, idx != nullptr);
     const int64_t slots = kMaxCtas + (int64_t)Tc * pool.Hkv * a.groups;
     char* p = static_cast<char*>(ws);
     a.pre = reinterpret_cast<uint64_t*>(p);
