@@ -846,6 +846,26 @@ def _scratch(ws: Optional["Workspace"], t: torch.Tensor, cur: int, nbytes: int, 
     return ws.buf
 
 
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output of a call on `stream`, whose memory is that stream's."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _beside(stream, cur: int, handle: int, *tensors) -> None:
+    """Tells the caching allocator that a call on a stream other than the current one uses these tensors, and
+    that the current one will use what the call gave them (their owner does not hold them for long enough)."""
+    if stream is None or handle == torch._C._cuda_getCurrentRawStream(cur) or torch.cuda.is_current_stream_capturing():
+        return
+    now = torch.cuda.current_stream(cur)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+            t.record_stream(now)
+
+
 def _address(buf) -> Optional[int]:
     return None if buf is None else buf.data_ptr()
 
@@ -927,12 +947,13 @@ def misa_kv4_append(k, v, pool, page_table, cu, start, k_scale: float = 1.0, v_s
     if Hp != H_kv:
         raise ValueError(f"the pool holds {Hp} kv heads, k has {H_kv}")
     cur = _current(k, "k")
-    code = _dtype_code(k)
+    code, h = _dtype_code(k), _handle(stream, cur)
     _check("misa_kv4_append", _lib.misa_kv4_append(
         _rows_ready(k, "k", k.dtype, cur), _rows_ready(v, "v", k.dtype, cur), ldk, ldv, code, k_scale, v_scale,
         _ready(pool, "pool", torch.uint8, cur), num_pages, page_size, _ready(page_table, "page_table", torch.int32, cur),
         max_pages, _ready(cu, "cu", torch.int32, cur), _ready(start, "start", torch.int32, cur), S, rows, H_kv, d,
-        _handle(stream, cur)))
+        h))
+    _beside(stream, cur, h, k, v, pool, page_table, cu, start)
 
 
 def misa_kv4_read(pool, page_table, cu, start, rows: int, d: int, dtype=torch.bfloat16, k_scale: float = 1.0,
@@ -948,12 +969,14 @@ def misa_kv4_read(pool, page_table, cu, start, rows: int, d: int, dtype=torch.bf
     pp, tp = _ready(pool, "pool", torch.uint8, cur), _ready(page_table, "page_table", torch.int32, cur)
     cp, sp = _ready(cu, "cu", torch.int32, cur), _ready(start, "start", torch.int32, cur)
     if k is None:
-        k = torch.empty((rows, H_kv, d), dtype=dtype, device=pool.device)
+        k = _new((rows, H_kv, d), dtype, pool.device, stream)
     if v is None:
-        v = torch.empty((rows, H_kv, d), dtype=dtype, device=pool.device)
+        v = _new((rows, H_kv, d), dtype, pool.device, stream)
+    h = _handle(stream, cur)
     _check("misa_kv4_read", _lib.misa_kv4_read(
         pp, num_pages, page_size, tp, max_pages, cp, sp, S, rows, H_kv, d, _dtype_code(k), k_scale, v_scale,
-        _ready(k, "k", dtype, cur), _ready(v, "v", dtype, cur), _handle(stream, cur)))
+        _ready(k, "k", dtype, cur), _ready(v, "v", dtype, cur), h))
+    _beside(stream, cur, h, k, v, pool, page_table, cu, start)
     return k, v
 
 
@@ -986,9 +1009,9 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
     ip, ap = _ready(idx, "idx", torch.int32, cur), _ready(acc, "acc", torch.float32, cur)
     P = 0 if idx is None else idx.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _new((T, H_q, d), q.dtype, q.device, stream)
     if lse is None and want_lse:
-        lse = torch.empty((T, H_q), dtype=torch.float32, device=q.device)
+        lse = _new((T, H_q), torch.float32, q.device, stream)
     h = _handle(stream, cur)
     nbytes = _ws_bytes(OP_KV4_ATTENTION, T, L, H_q, H_kv, d, P, int(acc is not None))
     buf = _scratch(ws, q, cur, nbytes, stream, h)
@@ -997,6 +1020,7 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
         d ** -0.5 if scale is None else scale, k_scale, v_scale, _ready(out, "out", q.dtype, cur),
         _ready(lse, "lse", torch.float32, cur), ap, 0 if acc is None else acc.shape[1],
         _address(buf), nbytes, h))
+    _beside(stream, cur, h, q, pool, page_table, n, idx, out, lse, acc)
     return out, lse
 
 
@@ -1019,15 +1043,17 @@ def misa_evict_select(acc, n, keep: int, sink: int = 0, recent: int = 0, L: Opti
     cur = _current(acc, "acc")
     ap, np_ = _ready(acc, "acc", torch.float32, cur), _ready(n, "n", torch.int32, cur)
     if idx is None:
-        idx = torch.empty((T, keep), dtype=torch.int32, device=acc.device)
+        idx = _new((T, keep), torch.int32, acc.device, stream)
     if n_out is None:
-        n_out = torch.empty((T,), dtype=torch.int32, device=acc.device)
+        n_out = _new((T,), torch.int32, acc.device, stream)
     if acc_out is None and want_acc:
-        acc_out = torch.empty((T, keep), dtype=torch.float32, device=acc.device)
+        acc_out = _new((T, keep), torch.float32, acc.device, stream)
+    h = _handle(stream, cur)
     _check("misa_evict_select", _lib.misa_evict_select(
         ap, ld, np_, T, L, keep, sink, recent, _ready(idx, "idx", torch.int32, cur),
         _ready(n_out, "n_out", torch.int32, cur), _ready(acc_out, "acc_out", torch.float32, cur),
-        0 if acc_out is None else acc_out.shape[1], _handle(stream, cur)))
+        0 if acc_out is None else acc_out.shape[1], h))
+    _beside(stream, cur, h, acc, n, idx, n_out, acc_out)
     return idx, n_out, acc_out
 
 
@@ -1046,6 +1072,7 @@ def misa_kv4_compact(pool, page_table, idx, d: int, ws: Optional[Workspace] = No
     _check("misa_kv4_compact", _lib.misa_kv4_compact(
         pp, num_pages, page_size, tp, max_pages, ip, T, keep, H_kv, d,
         _address(buf), nbytes, h))
+    _beside(stream, cur, h, pool, page_table, idx)
 
 
 def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = None, stream=None) -> None:
@@ -1067,6 +1094,7 @@ def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = Non
     _check("misa_keys_compact_paged", _lib.misa_keys_compact_paged(
         pp, num_pages, page_size, tp, page_table.shape[1], ip, T, keep, d, code,
         _address(buf), nbytes, h))
+    _beside(stream, cur, h, pool, page_table, idx)
 
 
 def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, lse=None,
@@ -1093,9 +1121,9 @@ def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = Non
     qp, kp, vp = _rows_ready(q, "q", bf, cur), _rows_ready(k, "k", bf, cur), _rows_ready(v, "v", bf, cur)
     cq, ck = _ready(cu_q, "cu_q", torch.int32, cur), _ready(cu_k, "cu_k", torch.int32, cur)
     if out is None:
-        out = torch.empty((Tq, H_q, d), dtype=bf, device=q.device)
+        out = _new((Tq, H_q, d), bf, q.device, stream)
     if lse is None and want_lse:
-        lse = torch.empty((Tq, H_q), dtype=torch.float32, device=q.device)
+        lse = _new((Tq, H_q), torch.float32, q.device, stream)
     h = _handle(stream, cur)
     nbytes = _ws_bytes(OP_PROMPT_ATTENTION, Tq, Tk, H_q, S, d, 0, 0)
     buf = _scratch(ws, q, cur, nbytes, stream, h)
@@ -1103,4 +1131,5 @@ def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = Non
         qp, kp, vp, ldq, ldk, ldv, cq, ck, S, Tq, Tk, H_q, H_kv, d, BF16, d ** -0.5 if scale is None else scale,
         _ready(out, "out", bf, cur), _ready(lse, "lse", torch.float32, cur),
         _address(buf), nbytes, h))
+    _beside(stream, cur, h, q, k, v, cu_q, cu_k, out, lse)
     return out, lse

@@ -162,3 +162,38 @@ def test_graphs_captured_without_a_workspace_replay_at_once():
         for s, o, w in zip(states, outs, want):
             assert all(torch.equal(x, y) for x, y in zip((*o, s["pool"], s["acc"]), w))
     M.misa_device_check()
+
+
+def test_calls_on_a_stream_beside_the_current_one():
+    """Outputs and inputs of a call on another stream: the memory of neither is handed out again too early."""
+    M = lib()
+    T, Hq, Hkv, d, page, cap = 8, 16, 2, 128, 64, 4096
+    gen = torch.Generator("cuda").manual_seed(9)
+    randn = lambda *s: torch.randn(*s, device="cuda", generator=gen).bfloat16()  # noqa: E731
+    table = torch.arange(T * cap // page, device="cuda", dtype=torch.int32).reshape(T, -1)
+    pool = M.misa_kv4_pool(T * cap // page, page, Hkv, d)
+    cu = torch.arange(T + 1, device="cuda", dtype=torch.int32) * cap
+    zero, n = torch.zeros(T, device="cuda", dtype=torch.int32), torch.full((T,), cap, device="cuda", dtype=torch.int32)
+    M.misa_kv4_append(randn(T * cap, Hkv, d), randn(T * cap, Hkv, d), pool, table, cu, zero)
+    q = randn(T, Hq, d)
+    pq, pk, pv = randn(2000, Hq, d), randn(2000, Hkv, d), randn(2000, Hkv, d)
+    pc = torch.tensor([0, 2000], device="cuda", dtype=torch.int32)
+    want = M.misa_kv4_attention(q, pool, table, n)[0].clone()
+    pwant = M.misa_prompt_attention(pq, pk, pv, pc)[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(20):
+        junk = torch.full((T, Hq, d), 3.0, device="cuda", dtype=torch.bfloat16)  # work on the current stream
+        junk.mul_(2.0)
+        del junk
+        q1 = q.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        o, _ = M.misa_kv4_attention(q1, pool, table, n, stream=side)
+        p, _ = M.misa_prompt_attention(pq, pk, pv, pc, stream=side)
+        del q1
+        torch.full((T, Hq, d), float("nan"), device="cuda", dtype=torch.bfloat16)  # as large as q1 was
+        outs.append((o, p))
+    torch.cuda.current_stream().wait_stream(side)
+    for o, p in outs:
+        assert torch.equal(o, want) and torch.equal(p, pwant)
