@@ -443,7 +443,8 @@ misa_status misa_keys_compact_paged(void* pool, int64_t num_pages, int page_size
  * Rows of other sequences never reach a sequence's outputs, whatever they hold, nor do keys and values
  * behind a query reach its own.
  *   ws     : misa_workspace_bytes(MISA_OP_PROMPT_ATTENTION, Tq, Tk, H_q, S, d, 0, 0) bytes (0 for a call of
- *            few short prompts; otherwise mostly the pieces of what is cut between CTAs, 40 MB at d = 128)
+ *            few short or many long prompts; otherwise mostly the pieces of what is cut between CTAs, 40 MB
+ *            at d = 128)
  */
 misa_status misa_prompt_attention(const void* q, const void* k, const void* v, int64_t ldq, int64_t ldk, int64_t ldv,
                                   const int32_t* cu_q, const int32_t* cu_k, int S, int Tq, int Tk, int H_q, int H_kv,
@@ -472,7 +473,8 @@ misa_status misa_device_check(void);
  * it lies outside its range is also counted on the device, by kind:
  *   out[0] routed head ids outside [0, H_I)            (scoring and block-filter calls)
  *   out[1] candidate token ids outside [0, n_t), other than the empty marker -1 (re-rank calls,
- *          paged or not, and attention over selected tokens; the header's "empty slot" rule still applies: they are skipped)
+ *          paged or not, and attention over selected tokens; the header's "empty slot" rule still
+ *          applies: they are skipped)
  *   out[2] page-table entries inside a prefix outside [0, num_pages) (paged calls; per key row
  *          read through the entry, in attention over a whole prefix per 16 of them)
  * The counts are occurrences seen, not distinct ids.  In both builds such ids are never
