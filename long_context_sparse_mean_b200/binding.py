@@ -857,7 +857,7 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
 def _beside(stream, cur: int, handle: int, *tensors) -> None:
     """Tells the caching allocator that a call on a stream other than the current one uses these tensors, and
     that the current one will use what the call gave them (their owner does not hold them for long enough)."""
-    if stream is None or handle == torch._C._cuda_getCurrentRawStream(cur) or torch.cuda.is_current_stream_capturing():
+    if handle == torch._C._cuda_getCurrentRawStream(cur) or torch.cuda.is_current_stream_capturing():
         return
     now = torch.cuda.current_stream(cur)
     for t in tensors:
@@ -953,7 +953,8 @@ def misa_kv4_append(k, v, pool, page_table, cu, start, k_scale: float = 1.0, v_s
         _ready(pool, "pool", torch.uint8, cur), num_pages, page_size, _ready(page_table, "page_table", torch.int32, cur),
         max_pages, _ready(cu, "cu", torch.int32, cur), _ready(start, "start", torch.int32, cur), S, rows, H_kv, d,
         h))
-    _beside(stream, cur, h, k, v, pool, page_table, cu, start)
+    if stream is not None:
+        _beside(stream, cur, h, k, v, pool, page_table, cu, start)
 
 
 def misa_kv4_read(pool, page_table, cu, start, rows: int, d: int, dtype=torch.bfloat16, k_scale: float = 1.0,
@@ -976,7 +977,8 @@ def misa_kv4_read(pool, page_table, cu, start, rows: int, d: int, dtype=torch.bf
     _check("misa_kv4_read", _lib.misa_kv4_read(
         pp, num_pages, page_size, tp, max_pages, cp, sp, S, rows, H_kv, d, _dtype_code(k), k_scale, v_scale,
         _ready(k, "k", dtype, cur), _ready(v, "v", dtype, cur), h))
-    _beside(stream, cur, h, k, v, pool, page_table, cu, start)
+    if stream is not None:
+        _beside(stream, cur, h, k, v, pool, page_table, cu, start)
     return k, v
 
 
@@ -1009,7 +1011,7 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
     ip, ap = _ready(idx, "idx", torch.int32, cur), _ready(acc, "acc", torch.float32, cur)
     P = 0 if idx is None else idx.shape[1]
     if out is None:
-        out = _new((T, H_q, d), q.dtype, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _new((T, H_q, d), q.dtype, q.device, stream)
     if lse is None and want_lse:
         lse = _new((T, H_q), torch.float32, q.device, stream)
     h = _handle(stream, cur)
@@ -1020,7 +1022,8 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
         d ** -0.5 if scale is None else scale, k_scale, v_scale, _ready(out, "out", q.dtype, cur),
         _ready(lse, "lse", torch.float32, cur), ap, 0 if acc is None else acc.shape[1],
         _address(buf), nbytes, h))
-    _beside(stream, cur, h, q, pool, page_table, n, idx, out, lse, acc)
+    if stream is not None:
+        _beside(stream, cur, h, q, pool, page_table, n, idx, out, lse, acc)
     return out, lse
 
 
@@ -1053,7 +1056,8 @@ def misa_evict_select(acc, n, keep: int, sink: int = 0, recent: int = 0, L: Opti
         ap, ld, np_, T, L, keep, sink, recent, _ready(idx, "idx", torch.int32, cur),
         _ready(n_out, "n_out", torch.int32, cur), _ready(acc_out, "acc_out", torch.float32, cur),
         0 if acc_out is None else acc_out.shape[1], h))
-    _beside(stream, cur, h, acc, n, idx, n_out, acc_out)
+    if stream is not None:
+        _beside(stream, cur, h, acc, n, idx, n_out, acc_out)
     return idx, n_out, acc_out
 
 
@@ -1072,7 +1076,8 @@ def misa_kv4_compact(pool, page_table, idx, d: int, ws: Optional[Workspace] = No
     _check("misa_kv4_compact", _lib.misa_kv4_compact(
         pp, num_pages, page_size, tp, max_pages, ip, T, keep, H_kv, d,
         _address(buf), nbytes, h))
-    _beside(stream, cur, h, pool, page_table, idx)
+    if stream is not None:
+        _beside(stream, cur, h, pool, page_table, idx)
 
 
 def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = None, stream=None) -> None:
@@ -1094,7 +1099,8 @@ def misa_keys_compact_paged(pool, page_table, idx, ws: Optional[Workspace] = Non
     _check("misa_keys_compact_paged", _lib.misa_keys_compact_paged(
         pp, num_pages, page_size, tp, page_table.shape[1], ip, T, keep, d, code,
         _address(buf), nbytes, h))
-    _beside(stream, cur, h, pool, page_table, idx)
+    if stream is not None:
+        _beside(stream, cur, h, pool, page_table, idx)
 
 
 def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = None, out=None, lse=None,
@@ -1131,5 +1137,6 @@ def misa_prompt_attention(q, k, v, cu_q, cu_k=None, scale: Optional[float] = Non
         qp, kp, vp, ldq, ldk, ldv, cq, ck, S, Tq, Tk, H_q, H_kv, d, BF16, d ** -0.5 if scale is None else scale,
         _ready(out, "out", bf, cur), _ready(lse, "lse", torch.float32, cur),
         _address(buf), nbytes, h))
-    _beside(stream, cur, h, q, k, v, cu_q, cu_k, out, lse)
+    if stream is not None:
+        _beside(stream, cur, h, q, k, v, cu_q, cu_k, out, lse)
     return out, lse
