@@ -407,7 +407,7 @@ misa_status misa_kv4_attention(const void* q, const void* pool, int64_t num_page
  * largest acc (ties: lower token; NaN counts as the smallest).
  *   acc         : [T][ld_acc] fp32, entries i < n_t are read (ld_acc >= L)
  *   idx         : out [T][keep] the tokens that stay, ascending, -1 behind the last
- *   n_out       : out [T] min(n_t, keep)
+ *   n_out       : out [T] min(n_t, keep); may be n itself (lengths updated in place), not overlap it otherwise
  *   acc_out_opt : out [T][ld_out] (ld_out >= keep): acc of the tokens that stay, in the order of idx,
  *                 then zeros to the end of the row; must not overlap acc.  Or NULL.
  */

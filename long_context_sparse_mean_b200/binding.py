@@ -1031,7 +1031,8 @@ def misa_evict_select(acc, n, keep: int, sink: int = 0, recent: int = 0, L: Opti
                       n_out=None, acc_out=None, want_acc: bool = False, stream=None):
     """Tokens that stay when every cache is thinned to `keep` by summed attention weight acc [T, >= L]:
     the first `sink`, the last `recent`, and the heaviest of the others -> (idx [T, keep] ascending and
-    -1 padded, n_out [T], acc_out [T, >= keep] the weights in that order and zeros behind them, or None)."""
+    -1 padded, n_out [T], acc_out [T, >= keep] the weights in that order and zeros behind them, or None).
+    n_out may be n itself: the lengths are then updated in place."""
     if acc.dim() != 2:
         raise ValueError(f"acc must be [T, ld], got {tuple(acc.shape)}")
     T, ld = acc.shape

@@ -140,6 +140,8 @@ misa_status misa_evict_select(const float* acc, int64_t ld_acc, const int32_t* n
                 *b1 = acc_out_opt + (int64_t)T * ld_out;
     if (a0 < b1 && b0 < a1) return MISA_ERR_INVALID_ARG;
   }
+  // the lengths may be updated in place, but no row may write another row's
+  if (n_out != n && n_out < n + T && n < n_out + T) return MISA_ERR_INVALID_ARG;
   misa::launch_evict_select(acc, ld_acc, n, T, L, keep, sink, recent, idx, n_out, acc_out_opt, ld_out,
                             static_cast<cudaStream_t>(stream));
   return launch_status();

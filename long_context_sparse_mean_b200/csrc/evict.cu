@@ -9,6 +9,7 @@
 // shared memory, and all add up the eight histograms through distributed shared memory.  Then every thread
 // counts the kept tokens of its run, one scan over the CTA and the counts of the CTAs before it say where they
 // go, and they are written in order.
+// n_out may be n: every thread of a row's CTAs reads its length before a barrier, the new one is written behind it.
 // 16 rows of up to 32768 tokens: 18.5 us (one CTA a row, with a scan for every 1024 tokens: 55.7; read in every
 // pass: 22); one row of 1000 tokens: 6.4 us.
 #include <cooperative_groups.h>
@@ -31,9 +32,9 @@ __device__ __forceinline__ uint32_t weight_key(float f) { return f == f ? order_
 
 template <int kCluster, int HOLD>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    evict_select_kernel(const float* __restrict__ acc, int64_t ld, const int32_t* __restrict__ n, int L, int keep,
-                        int sink, int recent, int32_t* __restrict__ idx, int32_t* __restrict__ n_out,
-                        float* __restrict__ acc_out, int64_t ld_out) {
+    evict_select_kernel(const float* __restrict__ acc, int64_t ld, const int32_t* n, int L, int keep, int sink,
+                        int recent, int32_t* __restrict__ idx, int32_t* n_out, float* __restrict__ acc_out,
+                        int64_t ld_out) {
   __shared__ __align__(16) uint32_t hist[3][kBins];
   __shared__ uint32_t warp_tot[32];
   __shared__ uint32_t found[2];
@@ -45,12 +46,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   const int kept = min(nt, keep);
   int32_t* out = idx + (int64_t)t * keep;
   float* aout = acc_out ? acc_out + (int64_t)t * ld_out : nullptr;
-  if (rank == 0 && threadIdx.x == 0) n_out[t] = kept;
   const int me = rank * kThreads + (int)threadIdx.x;
   for (int j = kept + me; j < keep; j += kCluster * kThreads) out[j] = -1;
   if (aout)
     for (int64_t j = kept + me; j < ld_out; j += kCluster * kThreads) aout[j] = 0.f;
   if (nt <= keep) {  // the whole cluster alike
+    if (kCluster > 1) cluster.sync();
+    else __syncthreads();
+    if (rank == 0 && threadIdx.x == 0) n_out[t] = kept;
     for (int s = me; s < nt; s += kCluster * kThreads) {
       out[s] = s;
       if (aout) aout[s] = __ldg(row + s);
@@ -157,6 +160,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     equal_at += eq;
   });
   if (kCluster > 1) cluster.sync();  // no CTA leaves while another may read its counts
+  if (rank == 0 && threadIdx.x == 0) n_out[t] = kept;
 }
 
 }  // namespace
