@@ -98,7 +98,8 @@ const char* misa_status_str(int status);
  * Workspace bytes needed by one call of `op` with these sizes (0 if it needs none).
  * Arguments an op does not use are ignored.  Sizes <= 0 give 0.  For MISA_OP_BLOCK_FILTER the
  * last argument carries m, the number of kept blocks (0 when m * B exceeds MISA_MAX_KP).  The calls
- * on 4-bit caches and compactions name what they put into these arguments themselves.
+ * on 4-bit caches, compactions and prompt attention name what they put into these arguments themselves;
+ * sizes that they refuse give 0.
  */
 size_t misa_workspace_bytes(int op, int T, int L, int H_I, int B, int h, int topk, int kp);
 

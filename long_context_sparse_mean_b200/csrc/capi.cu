@@ -207,15 +207,22 @@ size_t misa_workspace_bytes(int op, int T, int L, int H_I, int B, int h, int top
       return T > 0 && L > 0 && misa::fused_cap(topk) > 0 ? align_up(misa::fused_ws_bytes(T, L, topk)) : 0;
     case MISA_OP_HIER_FUSED:
       return hier_fused_ws(T, L, kp);
+    // The calls beside the indexer: 0 for sizes that they refuse, which are asked for before they can.
     case MISA_OP_KV4_ATTENTION:  // H_I query heads, B kv heads, h head width, topk selected tokens, kp weights
-      if (T <= 0 || L <= 0 || H_I <= 0 || B <= 0 || H_I % B != 0 || h <= 0) return 0;
+      if (T <= 0 || L <= 0 || L > misa::kMaxLen || topk > misa::kMaxLen || !misa::head_width(h)) return 0;
+      if (H_I <= 0 || H_I > misa::kMaxQueryHeads || B <= 0 || B > misa::kMaxKvHeads || H_I % B != 0) return 0;
       return misa::kv4_attention_ws_bytes(T, topk > 0 ? topk : L, H_I, B, h, kp != 0);
     case MISA_OP_KV4_COMPACT:  // H_I kv heads, h head width, topk kept tokens
-      return T > 0 && H_I > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, 2 * H_I, h / 2, h / 16) : 0;
-    case MISA_OP_PROMPT_ATTENTION:  // T queries, L keys, H_I query heads, B sequences, h head width
-      return H_I > 0 && h > 0 ? misa::prompt_ws_bytes(B, T, L, H_I, h) : 0;
+      if (T <= 0 || H_I <= 0 || H_I > misa::kMaxKvHeads || !misa::head_width(h) || topk <= 0 || topk > misa::kMaxLen)
+        return 0;
+      return misa::compact_ws_bytes(T, topk, 2 * H_I, h / 2, h / 16);
     case MISA_OP_KEYS_COMPACT_PAGED:  // h bytes of a key row, topk kept tokens
-      return T > 0 && h > 0 && topk > 0 ? misa::compact_ws_bytes(T, topk, 1, h, 0) : 0;
+      if (T <= 0 || (h != misa::kD * 2 && h != misa::kD * 4) || topk <= 0 || topk > misa::kMaxLen) return 0;
+      return misa::compact_ws_bytes(T, topk, 1, h, 0);
+    case MISA_OP_PROMPT_ATTENTION:  // T queries, L keys, H_I query heads, B sequences, h head width
+      if (H_I <= 0 || H_I > misa::kMaxPromptHeads || !misa::head_width(h) || T > misa::kMaxLen || L > misa::kMaxLen)
+        return 0;
+      return misa::prompt_ws_bytes(B, T, L, H_I, h);
     default:
       return 0;
   }

@@ -9,12 +9,12 @@
 #include "kernels.cuh"
 
 using misa::DType;
+using misa::kMaxLen;
 using misa::Kv4Pool;
 
 namespace {
 
 constexpr int kMaxPage = 1024;
-constexpr int kMaxLen = 1 << 30;
 
 bool at16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -28,8 +28,8 @@ DType to_dtype(int dtype) { return dtype == MISA_F32 ? DType::F32 : DType::BF16;
 // The sizes of a 4-bit pool and its page tables.
 misa_status check_kv4(int64_t num_pages, int page_size, int64_t max_pages, int H_kv, int d) {
   if (num_pages < 1 || page_size < 1 || max_pages < 1 || H_kv < 1) return MISA_ERR_INVALID_ARG;
-  if (d != 64 && d != 128) return MISA_ERR_UNSUPPORTED;
-  if (page_size % 16 != 0 || page_size > kMaxPage || H_kv > 1024) return MISA_ERR_UNSUPPORTED;
+  if (!misa::head_width(d)) return MISA_ERR_UNSUPPORTED;
+  if (page_size % 16 != 0 || page_size > kMaxPage || H_kv > misa::kMaxKvHeads) return MISA_ERR_UNSUPPORTED;
   if (num_pages > INT32_MAX / page_size || max_pages > INT32_MAX) return MISA_ERR_UNSUPPORTED;
   return MISA_OK;
 }
@@ -111,7 +111,7 @@ misa_status misa_kv4_attention(const void* q, const void* pool, int64_t num_page
   const misa_status st = check_kv4(num_pages, page_size, max_pages, H_kv, d);
   if (st != MISA_OK) return st;
   if (H_q % H_kv != 0 || (int64_t)L > max_pages * page_size) return MISA_ERR_INVALID_ARG;
-  if (L > kMaxLen || (idx && P > kMaxLen) || H_q > 65536) return MISA_ERR_UNSUPPORTED;
+  if (L > kMaxLen || (idx && P > kMaxLen) || H_q > misa::kMaxQueryHeads) return MISA_ERR_UNSUPPORTED;
   if (!positive(scale) || !factor(k_scale) || !factor(v_scale)) return MISA_ERR_INVALID_ARG;
   if (acc_opt && ld_acc < L) return MISA_ERR_INVALID_ARG;
   if (T == 0) return MISA_OK;
@@ -197,9 +197,9 @@ misa_status misa_prompt_attention(const void* q, const void* k, const void* v, i
                                   void* stream) {
   if (S < 0 || Tq < 0 || Tk < 0 || H_q < 1 || H_kv < 1) return MISA_ERR_INVALID_ARG;
   if (dtype != MISA_BF16) return MISA_ERR_UNSUPPORTED;
-  if (d != 64 && d != 128) return MISA_ERR_UNSUPPORTED;
+  if (!misa::head_width(d)) return MISA_ERR_UNSUPPORTED;
   if (H_q % H_kv != 0 || !positive(scale)) return MISA_ERR_INVALID_ARG;
-  if (Tq > kMaxLen || Tk > kMaxLen || H_q > 1024) return MISA_ERR_UNSUPPORTED;
+  if (Tq > kMaxLen || Tk > kMaxLen || H_q > misa::kMaxPromptHeads) return MISA_ERR_UNSUPPORTED;
   if (S == 0 || Tq == 0) return MISA_OK;
   if (!cu_q || !cu_k || !out || !at16(out)) return MISA_ERR_INVALID_ARG;
   misa_status st = check_rows(q, ldq, H_q, d, dtype);

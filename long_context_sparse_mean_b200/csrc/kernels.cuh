@@ -199,6 +199,11 @@ void launch_pool_paged(DType dt, const void* pool, int64_t num_pages, int page_s
 void launch_partial_mean_paged(DType dt, const void* pool, int64_t num_pages, int page_size, const int32_t* table,
                                int64_t max_pages, const int32_t* n, int T, int L, int B, float* pm, cudaStream_t s);
 
+// What the calls beside the indexer serve.
+constexpr int kMaxLen = 1 << 30;  // tokens of a sequence, rows of a packed tensor
+constexpr int kMaxQueryHeads = 65536, kMaxKvHeads = 1024, kMaxPromptHeads = 1024;
+inline bool head_width(int d) { return d == 64 || d == 128; }
+
 // Caches held in 4 bits (kv4_cache.cu; format and Kv4Pool in kv4.cuh).  Packed rows [rows] belong to
 // sequence b for cu[b] <= r < cu[b + 1] and to its logical positions start[b] + r - cu[b].
 void launch_kv4_append(DType dt, const void* k, const void* v, int64_t ldk, int64_t ldv, const Kv4Pool& pool,

@@ -30,3 +30,29 @@ def test_eviction_refuses_lengths_that_overlap_their_outputs(lib):
     for n_out in (0x20000 + 4, 0x20000 + 12, 0x20000 - 4, 0x20000 - 12):
         assert select(0x20000, n_out) == INVALID, hex(n_out)
     assert select(0x20000, 0x20000, T=0) == OK
+
+
+def test_workspace_of_widths_that_no_call_serves_is_zero(lib):
+    """Sizes are asked for before the call can refuse them: every width, head count and length gets an answer."""
+    ws = lib.misa_workspace_bytes
+    ATTEND, CLOSE_UP, KEYS, PROMPT = 11, 12, 13, 14
+    odd = (-(1 << 31), -64, -1, 0, 1, 2, 7, 8, 15, 16, 31, 32, 48, 63, 65, 72, 96, 127, 129, 192, 1 << 20, (1 << 31) - 1)
+    for h in odd + (256, 512):
+        assert ws(ATTEND, 4, 1000, 32, 8, h, 0, 1) == 0, h
+        assert ws(CLOSE_UP, 4, 0, 8, 0, h, 1000, 0) == 0, h
+        assert ws(PROMPT, 3000, 9000, 32, 2, h, 0, 0) == 0, h
+    for h in odd + (64, 128):
+        assert ws(KEYS, 4, 0, 0, 0, h, 1000, 0) == 0, h
+    for h in (64, 128):
+        assert ws(ATTEND, 4, 1000, 32, 8, h, 0, 1) > 0 and ws(CLOSE_UP, 4, 0, 8, 0, h, 1000, 0) > 0
+        assert ws(PROMPT, 3000, 9000, 32, 2, h, 0, 0) > 0
+        for many in (1025, 1 << 30, (1 << 31) - 1):  # heads
+            assert ws(CLOSE_UP, 4, 0, many, 0, h, 1000, 0) == 0 and ws(PROMPT, 3000, 9000, many, 2, h, 0, 0) == 0
+            assert ws(ATTEND, 4, 1000, many, many, h, 0, 0) == 0
+        assert ws(ATTEND, 4, 1000, 1 << 17, 8, h, 0, 0) == 0
+    for h in (256, 512):
+        assert ws(KEYS, 4, 0, 0, 0, h, 1000, 0) > 0
+    for far in ((1 << 30) + 1, (1 << 31) - 1):  # tokens
+        assert ws(ATTEND, 4, far, 32, 8, 128, 0, 0) == 0 and ws(ATTEND, 4, 1000, 32, 8, 128, far, 0) == 0
+        assert ws(CLOSE_UP, 4, 0, 8, 0, 128, far, 0) == 0 and ws(KEYS, 4, 0, 0, 0, 256, far, 0) == 0
+        assert ws(PROMPT, far, 9000, 32, 2, 128, 0, 0) == 0 and ws(PROMPT, 3000, far, 32, 2, 128, 0, 0) == 0
