@@ -402,6 +402,16 @@ misa_status misa_kv4_attention(const void* q, const void* pool, int64_t num_page
                                size_t ws_bytes, void* stream);
 
 /*
+ * misa_kv4_attention with an acc that has columns for the first acc_cols tokens only (1 <= acc_cols <= ld_acc;
+ * acc_cols need not reach L).  Later tokens are attended to alike; their weights are not kept.
+ */
+misa_status misa_kv4_attention_cols(const void* q, const void* pool, int64_t num_pages, int page_size,
+                                    const int32_t* page_table, int64_t max_pages, const int32_t* n, const int32_t* idx,
+                                    int T, int L, int P, int H_q, int H_kv, int d, int dtype, float scale,
+                                    float k_scale, float v_scale, void* out, float* lse_opt, float* acc_opt,
+                                    int acc_cols, int64_t ld_acc, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Which tokens stay when caches are thinned to `keep` tokens by the attention weight they have gathered
  * (acc of misa_kv4_attention).  Prefixes of at most keep tokens stay whole; of a longer one stay the
  * first `sink`, the last `recent` (sink + recent <= keep), and of those between the ones with the

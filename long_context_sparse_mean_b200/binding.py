@@ -77,6 +77,8 @@ def _setup(lib):
         "misa_kv4_read": ([P, i64, i32, P, i64, P, P, i32, i32, i32, i32, i32, f32, f32, P, P, P], i32),
         "misa_kv4_attention": ([P, P, i64, i32, P, i64, P, P, i32, i32, i32, i32, i32, i32, i32, f32, f32, f32, P, P,
                                 P, i64, P, sz, P], i32),
+        "misa_kv4_attention_cols": ([P, P, i64, i32, P, i64, P, P, i32, i32, i32, i32, i32, i32, i32, f32, f32, f32, P, P,
+                                     P, i32, i64, P, sz, P], i32),
         "misa_evict_select": ([P, i64, P, i32, i32, i32, i32, i32, P, P, P, i64, P], i32),
         "misa_kv4_compact": ([P, i64, i32, P, i64, P, i32, i32, i32, i32, P, sz, P], i32),
         "misa_keys_compact_paged": ([P, i64, i32, P, i64, P, i32, i32, i32, i32, P, sz, P], i32),
@@ -988,13 +990,16 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
     """Attention of one query token per sequence, q [T, H_q, d] (bf16 or fp32), over its 4-bit cache:
     over the whole prefix, or with idx [T, P] over the tokens listed there (the indexer's selection, -1
     for empty slots) -> (out [T, H_q, d], lse [T, H_q] or None).  scale defaults to 1 / sqrt(d).  acc
-    [T, >= L] fp32: every token's softmax weight, summed over the heads, is added to it."""
+    [T, >= L] fp32: every token's softmax weight, summed over the heads, is added to it.  L, the longest
+    prefix (a longer one is cut to it), defaults to what the page table reaches; acc may then end inside
+    the table's last page, where the weights of tokens behind its end are not kept."""
     if q.dim() != 3:
         raise ValueError(f"q must be [T, H_q, d], got {tuple(q.shape)}")
     T, H_q, d = q.shape
     num_pages, H_kv, page_size, max_pages = _kv4_geometry(pool, page_table, T, d)
-    if L is None:  # the longest prefix that the table (and acc) can hold
-        L = max_pages * page_size if acc is None else min(max_pages * page_size, acc.shape[-1])
+    reach = max_pages * page_size
+    cols = reach - page_size + 1 if L is None else L  # fewest columns of acc
+    L = reach if L is None else L
     _lengths(n, T)
     if idx is not None:
         _matrix(idx, "idx", T)
@@ -1003,7 +1008,7 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
     if lse is not None:
         _matrix(lse, "lse", T, H_q)
     if acc is not None:
-        _matrix(acc, "acc", T, min_cols=L)
+        _matrix(acc, "acc", T, min_cols=cols)
     cur = _current(q, "q")
     code = _dtype_code(q)
     qp, pp = _ready(q, "q", q.dtype, cur), _ready(pool, "pool", torch.uint8, cur)
@@ -1017,11 +1022,11 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
     h = _handle(stream, cur)
     nbytes = _ws_bytes(OP_KV4_ATTENTION, T, L, H_q, H_kv, d, P, int(acc is not None))
     buf = _scratch(ws, q, cur, nbytes, stream, h)
-    _check("misa_kv4_attention", _lib.misa_kv4_attention(
+    ld = 0 if acc is None else acc.shape[1]
+    _check("misa_kv4_attention", _lib.misa_kv4_attention_cols(
         qp, pp, num_pages, page_size, tp, max_pages, np_, ip, T, L, P, H_q, H_kv, d, code,
         d ** -0.5 if scale is None else scale, k_scale, v_scale, _ready(out, "out", q.dtype, cur),
-        _ready(lse, "lse", torch.float32, cur), ap, 0 if acc is None else acc.shape[1],
-        _address(buf), nbytes, h))
+        _ready(lse, "lse", torch.float32, cur), ap, min(L, ld), ld, _address(buf), nbytes, h))
     if stream is not None:
         _beside(stream, cur, h, q, pool, page_table, n, idx, out, lse, acc)
     return out, lse
@@ -1032,7 +1037,9 @@ def misa_evict_select(acc, n, keep: int, sink: int = 0, recent: int = 0, L: Opti
     """Tokens that stay when every cache is thinned to `keep` by summed attention weight acc [T, >= L]:
     the first `sink`, the last `recent`, and the heaviest of the others -> (idx [T, keep] ascending and
     -1 padded, n_out [T], acc_out [T, >= keep] the weights in that order and zeros behind them, or None).
-    n_out may be n itself: the lengths are then updated in place."""
+    n_out may be n itself: the lengths are then updated in place.  L defaults to acc's width; a longer
+    prefix is cut to it, its last tokens lost.  To go on summing, give an acc_out as wide as acc:
+    want_acc makes one of keep columns, which has none for the tokens appended next."""
     if acc.dim() != 2:
         raise ValueError(f"acc must be [T, ld], got {tuple(acc.shape)}")
     T, ld = acc.shape

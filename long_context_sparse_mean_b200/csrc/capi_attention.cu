@@ -106,6 +106,15 @@ misa_status misa_kv4_attention(const void* q, const void* pool, int64_t num_page
                                int T, int L, int P, int H_q, int H_kv, int d, int dtype, float scale, float k_scale,
                                float v_scale, void* out, float* lse_opt, float* acc_opt, int64_t ld_acc, void* ws,
                                size_t ws_bytes, void* stream) {
+  return misa_kv4_attention_cols(q, pool, num_pages, page_size, page_table, max_pages, n, idx, T, L, P, H_q, H_kv, d,
+                                 dtype, scale, k_scale, v_scale, out, lse_opt, acc_opt, L, ld_acc, ws, ws_bytes, stream);
+}
+
+misa_status misa_kv4_attention_cols(const void* q, const void* pool, int64_t num_pages, int page_size,
+                                    const int32_t* page_table, int64_t max_pages, const int32_t* n, const int32_t* idx,
+                                    int T, int L, int P, int H_q, int H_kv, int d, int dtype, float scale,
+                                    float k_scale, float v_scale, void* out, float* lse_opt, float* acc_opt,
+                                    int acc_cols, int64_t ld_acc, void* ws, size_t ws_bytes, void* stream) {
   if (T < 0 || L < 1 || H_q < 1 || (idx && P < 1)) return MISA_ERR_INVALID_ARG;
   if (dtype != MISA_BF16 && dtype != MISA_F32) return MISA_ERR_UNSUPPORTED;
   const misa_status st = check_kv4(num_pages, page_size, max_pages, H_kv, d);
@@ -113,7 +122,7 @@ misa_status misa_kv4_attention(const void* q, const void* pool, int64_t num_page
   if (H_q % H_kv != 0 || (int64_t)L > max_pages * page_size) return MISA_ERR_INVALID_ARG;
   if (L > kMaxLen || (idx && P > kMaxLen) || H_q > misa::kMaxQueryHeads) return MISA_ERR_UNSUPPORTED;
   if (!positive(scale) || !factor(k_scale) || !factor(v_scale)) return MISA_ERR_INVALID_ARG;
-  if (acc_opt && ld_acc < L) return MISA_ERR_INVALID_ARG;
+  if (acc_opt && (acc_cols < 1 || ld_acc < acc_cols)) return MISA_ERR_INVALID_ARG;
   if (T == 0) return MISA_OK;
   if (!q || !at16(q) || !pool || !at16(pool) || !page_table || !n || !out || !at16(out)) return MISA_ERR_INVALID_ARG;
   const int seen = idx ? P : L;
@@ -121,8 +130,8 @@ misa_status misa_kv4_attention(const void* q, const void* pool, int64_t num_page
       (reinterpret_cast<uintptr_t>(ws) & 255))
     return MISA_ERR_WORKSPACE;
   misa::launch_kv4_attention(to_dtype(dtype), q, to_pool(pool, num_pages, page_size, page_table, max_pages, H_kv, d), n,
-                             idx, T, L, seen, H_q, scale, k_scale, v_scale, out, lse_opt, acc_opt, ld_acc, ws,
-                             static_cast<cudaStream_t>(stream));
+                             idx, T, L, seen, H_q, scale, k_scale, v_scale, out, lse_opt, acc_opt, acc_cols, ld_acc,
+                             ws, static_cast<cudaStream_t>(stream));
   return launch_status();
 }
 

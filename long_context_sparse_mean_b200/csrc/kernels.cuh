@@ -219,11 +219,11 @@ bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, i
                          int T, int keep, void* ws, cudaStream_t s);
 
 // Attention of query t over its sequence's tokens in a 4-bit cache, or over the tokens idx[t][0 .. P)
-// (kv4_attn.cu).  acc (optional): acc[t, i] += sum over heads of token i's weight.
+// (kv4_attn.cu).  acc (optional): acc[t, i] += sum over heads of token i's weight, for i < acc_cols.
 size_t kv4_attention_ws_bytes(int T, int P, int Hq, int Hkv, int d, bool weights);
 void launch_kv4_attention(DType dt, const void* q, const Kv4Pool& pool, const int32_t* n, const int32_t* idx, int T,
                           int L, int P, int Hq, float scale, float k_scale, float v_scale, void* out, float* lse,
-                          float* acc, int64_t ld_acc, void* ws, cudaStream_t s);
+                          float* acc, int acc_cols, int64_t ld_acc, void* ws, cudaStream_t s);
 
 // The tokens that stay when caches are thinned by summed attention weight (evict.cu).
 void launch_evict_select(const float* acc, int64_t ld, const int32_t* n, int T, int L, int keep, int sink, int recent,

@@ -790,12 +790,13 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const AttnArgs a, int HB,
   }
 }
 
-// acc[t, i] += sum over the heads of token i's weight, from the logits and every head's log-sum.  SHARE threads
+// acc[t, i] += sum over the heads of token i's weight, i < cols, from the logits and every head's log-sum.  SHARE threads
 // a position, each every SHARE-th head, and their sums in order.
 // Selected tokens are added atomically: a token that a list names twice gets both of its (equal)
 // weights, in either order the same sum.
 template <int SHARE>
-__global__ void __launch_bounds__(256) kv4_weights_kernel(const AttnArgs a, float* __restrict__ acc, int64_t ld) {
+__global__ void __launch_bounds__(256)
+    kv4_weights_kernel(const AttnArgs a, float* __restrict__ acc, int cols, int64_t ld) {
   constexpr int kTokens = 256 / SHARE;
   __shared__ float part[SHARE][kTokens];
   pdl_wait();
@@ -803,7 +804,7 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const AttnArgs a, floa
   const int x = threadIdx.x % kTokens, y = threadIdx.x / kTokens, p = blockIdx.x * kTokens + x;
   int s = p < (a.idx ? a.P : nt) ? p : -1;
   if (a.idx && s >= 0) s = __ldg(a.idx + (int64_t)t * a.P + p);
-  const bool there = s >= 0 && s < nt;
+  const bool there = s >= 0 && s < min(nt, cols);
   float w = 0.f;
   if (there) {
     const float* row = a.logits + (int64_t)t * a.Hq * a.ldS + p;
@@ -840,7 +841,7 @@ int64_t attn_ctas(int T, int P, int Hkv, int G, bool selected) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 template <int D, int NT, int SPLIT>
-void launch_attn(const AttnArgs& a, float* acc, int64_t ld_acc, int64_t ctas, cudaStream_t s) {
+void launch_attn(const AttnArgs& a, float* acc, int cols, int64_t ld_acc, int64_t ctas, cudaStream_t s) {
   if (ctas > 0) {
     if (a.idx) kv4_attn_kernel<D, NT, SPLIT, true><<<(unsigned)ctas, kThreads, 0, s>>>(a);
     else kv4_attn_kernel<D, NT, SPLIT, false><<<(unsigned)ctas, kThreads, 0, s>>>(a);
@@ -855,7 +856,7 @@ void launch_attn(const AttnArgs& a, float* acc, int64_t ld_acc, int64_t ctas, cu
     // few positions do not fill the GPU with a thread each: 32 x 2048 selected ones take 9 us for 15 with four;
     // 32 x 16384 take 10 us, with four 14
     auto weights = [&](auto kernel, int tokens) {
-      launch_pdl(kernel, dim3((a.P + tokens - 1) / tokens, a.T), dim3(256), 0, s, a, acc, ld_acc);
+      launch_pdl(kernel, dim3((a.P + tokens - 1) / tokens, a.T), dim3(256), 0, s, a, acc, cols, ld_acc);
     };
     if ((int64_t)a.T * a.P <= 148 * 1024) weights(kv4_weights_kernel<4>, 64);
     else weights(kv4_weights_kernel<1>, 256);
@@ -878,7 +879,7 @@ size_t kv4_attention_ws_bytes(int T, int P, int Hq, int Hkv, int d, bool weights
 
 void launch_kv4_attention(DType dt, const void* q, const Kv4Pool& pool, const int32_t* n, const int32_t* idx, int T,
                           int L, int P, int Hq, float scale, float k_scale, float v_scale, void* out, float* lse,
-                          float* acc, int64_t ld_acc, void* ws, cudaStream_t s) {
+                          float* acc, int acc_cols, int64_t ld_acc, void* ws, cudaStream_t s) {
   const int G = Hq / pool.Hkv, HB = heads_per_item(G);
   const size_t elt = dt == DType::BF16 ? 2 : 4;
   for (int t0 = 0; t0 < T; t0 += kMaxT) {
@@ -922,12 +923,13 @@ void launch_kv4_attention(DType dt, const void* q, const Kv4Pool& pool, const in
       ac = acc + (int64_t)t0 * ld_acc;
     }
     const bool f32 = dt == DType::F32;
+    auto run = [&](auto launch) { launch(a, ac, acc_cols, ld_acc, ctas, s); };
     if (pool.d == 128) {
-      if (HB == 8) f32 ? launch_attn<128, 1, 2>(a, ac, ld_acc, ctas, s) : launch_attn<128, 1, 1>(a, ac, ld_acc, ctas, s);
-      else f32 ? launch_attn<128, 2, 2>(a, ac, ld_acc, ctas, s) : launch_attn<128, 2, 1>(a, ac, ld_acc, ctas, s);
+      if (HB == 8) f32 ? run(launch_attn<128, 1, 2>) : run(launch_attn<128, 1, 1>);
+      else f32 ? run(launch_attn<128, 2, 2>) : run(launch_attn<128, 2, 1>);
     } else {
-      if (HB == 8) f32 ? launch_attn<64, 1, 2>(a, ac, ld_acc, ctas, s) : launch_attn<64, 1, 1>(a, ac, ld_acc, ctas, s);
-      else f32 ? launch_attn<64, 2, 2>(a, ac, ld_acc, ctas, s) : launch_attn<64, 2, 1>(a, ac, ld_acc, ctas, s);
+      if (HB == 8) f32 ? run(launch_attn<64, 1, 2>) : run(launch_attn<64, 1, 1>);
+      else f32 ? run(launch_attn<64, 2, 2>) : run(launch_attn<64, 2, 1>);
     }
   }
 }

@@ -2,10 +2,11 @@
 import ctypes
 
 import pytest
+import torch
 
 from long_context_sparse_mean_b200 import build
 
-OK, INVALID = 0, 1
+OK, INVALID, UNSUPPORTED, WORKSPACE = range(4)
 P = ctypes.c_void_p
 FAKE = P(0x10000)  # never dereferenced: every call below fails validation first
 
@@ -56,3 +57,23 @@ def test_workspace_of_widths_that_no_call_serves_is_zero(lib):
         assert ws(ATTEND, 4, far, 32, 8, 128, 0, 0) == 0 and ws(ATTEND, 4, 1000, 32, 8, 128, far, 0) == 0
         assert ws(CLOSE_UP, 4, 0, 8, 0, 128, far, 0) == 0 and ws(KEYS, 4, 0, 0, 0, 256, far, 0) == 0
         assert ws(PROMPT, far, 9000, 32, 2, 128, 0, 0) == 0 and ws(PROMPT, 3000, far, 32, 2, 128, 0, 0) == 0
+
+
+def test_attention_refuses_sums_that_end_before_the_last_page(M, lib):
+    """Without L a prefix may be as long as the table reaches, so acc has to reach the table's last page."""
+    zeros = lambda *s, dtype=torch.int32: torch.zeros(s, dtype=dtype)  # noqa: E731
+    pool, table, n = zeros(12, 2, 2, 16 * 72, dtype=torch.uint8), zeros(3, 4), zeros(3)
+    q = zeros(3, 8, 128, dtype=torch.bfloat16)
+    for cols, what in ((10, "acc must be"), (48, "acc must be"), (49, "CUDA tensor"), (64, "CUDA tensor"), (99, "CUDA tensor")):
+        with pytest.raises(ValueError, match=what):
+            M.misa_kv4_attention(q, pool, table, n, acc=zeros(3, cols, dtype=torch.float32))
+    for cols, what in ((39, "acc must be"), (40, "CUDA tensor")):
+        with pytest.raises(ValueError, match=what):
+            M.misa_kv4_attention(q, pool, table, n, acc=zeros(3, cols, dtype=torch.float32), L=40)
+
+    def attend(cols, ld, acc=FAKE, ws=None):
+        return lib.misa_kv4_attention_cols(FAKE, FAKE, 100, 64, FAKE, 10, FAKE, None, 4, 640, 0, 32, 8, 128, 0, 0.1, 1.0, 1.0,
+                                           FAKE, None, acc, cols, ld, ws, 0, None)
+
+    assert attend(0, 100) == INVALID and attend(-1, 100) == INVALID and attend(101, 100) == INVALID
+    assert attend(100, 100) == WORKSPACE and attend(0, 0, acc=None) == WORKSPACE  # nothing to refuse but the scratch

@@ -35,3 +35,48 @@ def test_lengths_updated_in_place(lens, keep):
         m = n.clone()
         got = M.misa_evict_select(acc, m, keep, 3, 40, n_out=m, want_acc=True)
         assert got[1] is m and all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def serving_state(M, lens, page, per, Hkv, d, seed):
+    """Caches of these lengths behind shuffled tables of `per` pages a sequence."""
+    gen = torch.Generator("cuda").manual_seed(seed)
+    T = len(lens)
+    table = torch.randperm(T * per, device="cuda", generator=gen).int().view(T, per)
+    pool = M.misa_kv4_pool(T * per, page, Hkv, d)
+    cu = cuda(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+    k, v = (torch.randn(sum(lens), Hkv, d, device="cuda", generator=gen).bfloat16() for _ in range(2))
+    M.misa_kv4_append(k, v, pool, table, cu, cuda(np.zeros(T, np.int32)))
+    return pool, table, cuda(np.array(lens, np.int32)), gen
+
+
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("selected", [False, True])
+def test_tokens_appended_after_an_eviction_are_attended_to(wide, selected):
+    """Summed weights that end before the table does change nothing in the attention of later tokens."""
+    M = lib()
+    Hq, Hkv, d, page, per, keep = 8, 2, 128, 16, 4, 50
+    pool, table, n, gen = serving_state(M, [60, 40, 64], page, per, Hkv, d, 3)
+    T = 3
+    acc = torch.rand(T, per * page, device="cuda", generator=gen)
+    room = torch.empty_like(acc) if wide else None
+    idx, n, acc = M.misa_evict_select(acc, n, keep, 2, 9, acc_out=room, want_acc=not wide)
+    M.misa_kv4_compact(pool, table, idx, d)
+    assert tuple(acc.shape) == (T, per * page if wide else keep)
+    one = torch.arange(T + 1, device="cuda", dtype=torch.int32)
+    full = torch.zeros(T, per * page, device="cuda")
+    full[:, :acc.shape[1]] = acc
+    for step in range(9):
+        k, v = (torch.randn(T, Hkv, d, device="cuda", generator=gen).bfloat16() for _ in range(2))
+        M.misa_kv4_append(k, v, pool, table, one, n)
+        n.add_(1)
+        q = torch.randn(T, Hq, d, device="cuda", generator=gen).bfloat16()
+        pick = None
+        if selected:  # the newest token first
+            pick = (n[:, None] - 1 - 7 * torch.arange(6, device="cuda", dtype=torch.int32)[None]).int().contiguous()
+        want, lse = M.misa_kv4_attention(q, pool, table, n, idx=pick, acc=full, want_lse=True)
+        bare, _ = M.misa_kv4_attention(q, pool, table, n, idx=pick)
+        out, z = M.misa_kv4_attention(q, pool, table, n, idx=pick, acc=acc, want_lse=True)
+        assert torch.equal(out, want) and torch.equal(z, lse) and torch.equal(bare, want), step
+        assert torch.equal(acc, full[:, :acc.shape[1]]), step
+    sums = (full.sum(1) - full[:, :keep].sum(1))
+    assert (sums[[0, 2]] > 0).all(), "tokens past the sums' columns were attended to"
