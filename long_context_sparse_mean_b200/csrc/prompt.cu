@@ -480,9 +480,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + L::kOffMisc);
   volatile uint32_t* tmem_slot = misc;
   volatile int* abort = reinterpret_cast<volatile int*>(misc + 1);
-  // segment (plus one) in which a value that is not finite was set to zero, by its number modulo 4: guards
-  // and softmax are never as far apart
-  volatile int* odd = reinterpret_cast<volatile int*>(misc + 4);
+  // the last segment (plus one) in which a value that is not finite was set to zero, for every residue of its
+  // number modulo 4.  It only grows, so that guards that are ahead of the softmax, by any number of segments,
+  // cannot hide what they did in the softmax's own; what they did later costs it a search for nothing.
+  int* odd = reinterpret_cast<int*>(misc + 4);
   Pair* found = reinterpret_cast<Pair*>(misc + 8);
   uint32_t* warp_tot = misc + 20;
   int* hit = reinterpret_cast<int*>(misc + 2);
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           a.lse[((int64_t)p.row + i) * a.Hq + walk.head] =
               l == 0.f ? -INFINITY : m * c * 0.693147180559945309f + logf(l);
         }
-        if (odd[seg & 3] == seg + 1 && i < p.rows)
+        if (*reinterpret_cast<volatile int*>(odd + (seg & 3)) > seg && i < p.rows)
           add_strange<D>(a.v + (int64_t)p.key0 * a.ldv + (walk.head / a.G) * D, a.ldv, p, from, to_, i,
                          whole ? out : nullptr, part);
       }
@@ -933,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               changed = bad = true;
             }
           }
-          if (bad) odd[seg & 3] = seg + 1;
+          if (bad) atomicMax(odd + (seg & 3), seg + 1);
           if (changed) tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(vok(b));

@@ -80,3 +80,40 @@ def test_tokens_appended_after_an_eviction_are_attended_to(wide, selected):
         assert torch.equal(acc, full[:, :acc.shape[1]]), step
     sums = (full.sum(1) - full[:, :keep].sum(1))
     assert (sums[[0, 2]] > 0).all(), "tokens past the sums' columns were attended to"
+
+
+@pytest.mark.parametrize("junk", [float("inf"), float("nan")])
+@pytest.mark.parametrize("d,Hq,Hkv,S,longest", [
+    (64, 4, 2, 400, 128),    # a block a prompt: the guards are prompts ahead of the outputs
+    (128, 3, 1, 400, 128),
+    (64, 3, 3, 260, 300),    # both tiles, and prompts that one tile has alone
+    (128, 2, 1, 700, 40),
+])
+def test_values_that_are_not_finite_in_neighbouring_prompts(junk, d, Hq, Hkv, S, longest):
+    """Short prompts share CTAs, some of them without a key: the rows that see such a value, and only they, have it."""
+    M = lib()
+    rng = np.random.default_rng(S + d)
+    keys = rng.integers(1, longest + 1, S)
+    queries = keys.copy()
+    for b in range(S):  # one to four prompts of ten that see nothing, one after another
+        if b % 10 in ((2,), (2, 3), (2, 3, 4), (2, 3, 4, 5))[b // 10 % 4]:
+            keys[b] = 0
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (queries, keys))
+    q = cuda(rng.standard_normal((cu_q[-1], Hq, d)).astype(np.float32), torch.bfloat16)
+    k, v = (cuda(rng.standard_normal((cu_k[-1], Hkv, d)).astype(np.float32), torch.bfloat16) for _ in range(2))
+    args = (cuda(cu_q), cuda(cu_k))
+    good, gl = M.misa_prompt_attention(q, k, v, *args, want_lse=True)
+    assert torch.isfinite(good.float()).all()
+    want = good.clone()
+    for b in range(S):
+        if keys[b] == 0 or b % 7 == 0:
+            continue
+        at, e, h = int(rng.integers(keys[b])), int(rng.integers(d)), int(rng.integers(Hkv))
+        v[cu_k[b] + at, h, e] = junk
+        G = Hq // Hkv
+        want[cu_q[b] + at:cu_q[b + 1], h * G:(h + 1) * G, e] = junk
+    for _ in range(10):
+        out, lse = M.misa_prompt_attention(q, k, v, *args, want_lse=True)
+        assert torch.equal(torch.nan_to_num(out.float(), nan=-7e9, posinf=7e9), torch.nan_to_num(want.float(), nan=-7e9, posinf=7e9))
+        assert torch.equal(lse, gl)
+    M.misa_device_check()
