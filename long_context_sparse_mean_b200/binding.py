@@ -1002,7 +1002,7 @@ def misa_kv4_attention(q, pool, page_table, n, idx=None, L: Optional[int] = None
     L = reach if L is None else L
     _lengths(n, T)
     if idx is not None:
-        _matrix(idx, "idx", T)
+        _matrix(idx, "idx", T, min_cols=1)  # a list of no width has no address and would mean the whole prefix
     if out is not None and tuple(out.shape) != (T, H_q, d):
         raise ValueError(f"out must be {[T, H_q, d]}, got {tuple(out.shape)}")
     if lse is not None:

@@ -77,3 +77,12 @@ def test_attention_refuses_sums_that_end_before_the_last_page(M, lib):
 
     assert attend(0, 100) == INVALID and attend(-1, 100) == INVALID and attend(101, 100) == INVALID
     assert attend(100, 100) == WORKSPACE and attend(0, 0, acc=None) == WORKSPACE  # nothing to refuse but the scratch
+
+
+def test_attention_refuses_a_selection_without_columns(M):
+    """An empty tensor has no address, which the library takes for 'no selection, the whole prefix'."""
+    zeros = lambda *s, dtype=torch.int32: torch.zeros(s, dtype=dtype)  # noqa: E731
+    pool, q = zeros(12, 2, 2, 16 * 72, dtype=torch.uint8), zeros(3, 8, 128, dtype=torch.bfloat16)
+    assert zeros(3, 0).data_ptr() == 0
+    with pytest.raises(ValueError, match="idx must be"):
+        M.misa_kv4_attention(q, pool, zeros(3, 4), zeros(3), idx=zeros(3, 0))
