@@ -434,7 +434,7 @@ misa_status misa_evict_select(const float* acc, int64_t ld_acc, const int32_t* n
  * T sequences must be theirs alone.
  *   ws : misa_workspace_bytes(MISA_OP_KV4_COMPACT, T, 0, H_kv, 0, d, keep, 0), and
  *        misa_workspace_bytes(MISA_OP_KEYS_COMPACT_PAGED, T, 0, 0, 0, bytes of a key row, keep, 0) bytes
- *        (marks of which rows have been read; cleared by the call)
+ *        (marks of which rows have been read, and counters of who reads which; cleared by the call)
  */
 misa_status misa_kv4_compact(void* pool, int64_t num_pages, int page_size, const int32_t* page_table,
                              int64_t max_pages, const int32_t* idx, int T, int keep, int H_kv, int d, void* ws,

@@ -213,7 +213,8 @@ void launch_kv4_read(DType dt, const Kv4Pool& pool, const int32_t* cu, const int
 // Closes up the rows of every sequence in place: row idx[t, j] moves to row j (idx ascending, -1 behind
 // the last).  Rows of a page are rb bytes in each of `slabs` slabs of slab_bytes, and behind those
 // page_size scale rows of sb bytes (0, 4 or 8).
-// ws: one mark per sequence, group of slabs and segment of rows (cleared by the call).
+// ws: one mark per sequence, group of slabs and segment of rows, and a counter per sequence and group (cleared by
+// the call).
 size_t compact_ws_bytes(int T, int keep, int slabs, int rb, int sb);
 bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, int rb, int sb, const int32_t* idx,
                          int T, int keep, void* ws, cudaStream_t s);

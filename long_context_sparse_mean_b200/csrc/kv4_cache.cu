@@ -223,10 +223,11 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Pool pool, const int32
 // of R rows j of one sequence and a group of slabs: it reads their sources into shared memory, marks its
 // segment as read, waits until every segment whose sources lie where it is going to write has been
 // marked, and writes.  idx is ascending, so idx[t, j] >= j: a segment's own place is read by itself and by
-// segments before it alone, which have smaller block indices, started no later, and wait for none after
-// them; they are found by searching idx for the ends of the place while the copies are under way.  (In
-// the usual case of a part kept, rows come from far behind their new place, and the segments waited for
-// finished long ago.)  A short list is one segment and needs no marks.
+// segments before it alone; they are found by searching idx for the ends of the place while the copies are
+// under way.  Segments are handed out in order by a counter of each sequence and group, not by block index, so
+// that those before a CTA's own are with CTAs that run already, whatever order CTAs start in, and a segment
+// is marked before its CTA waits for any.  (In the usual case of a part kept, rows come from far behind their
+// new place, and the segments waited for finished long ago.)  A short list is one segment and needs no marks.
 // Rows that stay where they are are passed over, and so are rows whose own or source page is not in the
 // pool.  Bound by HBM: rows are read and written once, but rows of 64 and 8 bytes from here and there fetch up
 // to twice their size.  16 caches of up to 32768 tokens thinned to 8192 (8 heads of 128): 60 us for 85 MB moved,
@@ -277,11 +278,15 @@ __global__ void __launch_bounds__(kCompactThreads) compact_rows_kernel(RowPages 
                                                                        int64_t stride, int row_bytes, int64_t page_bytes,
                                                                        int64_t scales_at, int sb,
                                                                        const int32_t* __restrict__ idx, int keep, int R,
-                                                                       uint32_t* __restrict__ read_marks) {
+                                                                       uint32_t* read_marks, uint32_t* turns) {
   constexpr int rb = 16 * P;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int first_wait, end_wait, late;
-  const int seg = blockIdx.x, t = blockIdx.z, s0 = blockIdx.y * group, ns = min(group, slabs - s0);
+  __shared__ int first_wait, end_wait, late, turn;
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) turn = (int)atomicAdd(turns + (int64_t)blockIdx.z * gridDim.y + blockIdx.y, 1u);
+    __syncthreads();
+  }
+  const int seg = gridDim.x > 1 ? turn : 0, t = blockIdx.z, s0 = blockIdx.y * group, ns = min(group, slabs - s0);
   const int j0 = seg * R, warp = threadIdx.x >> 5;
   const int32_t* list = idx + (int64_t)t * keep;
   uint32_t* marks = read_marks + ((int64_t)t * gridDim.y + blockIdx.y) * gridDim.x;
@@ -413,6 +418,9 @@ CompactPlan compact_plan(int T, int slabs, int rb, int sb, int keep) {
   return p;
 }
 
+// A mark for every segment, and behind them the segments handed out of every sequence and group.
+size_t ws_words(int T, const CompactPlan& p) { return (size_t)T * p.groups * (p.segs + 1); }
+
 }  // namespace
 
 void launch_kv4_append(DType dt, const void* k, const void* v, int64_t ldk, int64_t ldv, const Kv4Pool& pool,
@@ -437,7 +445,7 @@ size_t compact_ws_bytes(int T, int keep, int slabs, int row, int sb) {
   const int rb = sb ? row : 64;
   slabs *= row / rb;
   const CompactPlan p = compact_plan(T, slabs, rb, sb, keep);
-  return sizeof(uint32_t) * (size_t)T * p.groups * p.segs;
+  return ws_words(T, p) * sizeof(uint32_t);
 }
 
 bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, int row, int sb, const int32_t* idx,
@@ -448,8 +456,9 @@ bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, i
   const int rb = sb ? row : 64;
   slabs *= row / rb;
   const CompactPlan p = compact_plan(T, slabs, rb, sb, keep);
-  if (p.segs > 1 && cudaMemsetAsync(ws, 0, sizeof(uint32_t) * (size_t)T * p.groups * p.segs, s) != cudaSuccess)
-    return false;
+  uint32_t* const marks = static_cast<uint32_t*>(ws);
+  uint32_t* const turns = marks + (size_t)T * p.groups * p.segs;
+  if (p.segs > 1 && cudaMemsetAsync(ws, 0, sizeof(uint32_t) * ws_words(T, p), s) != cudaSuccess) return false;
   auto run = [&](auto kernel) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOneSegBytes + 16384) != cudaSuccess)
       return false;
@@ -459,7 +468,7 @@ bool launch_compact_rows(const RowPages& pages, int slabs, int64_t slab_bytes, i
       q.table += (int64_t)t0 * pages.max_pages;
       kernel<<<dim3(p.segs, p.groups, std::min(T - t0, kMostZ)), kCompactThreads, p.smem, s>>>(
           q, slabs, p.group, stride, row, page_bytes, scales_at, sb, idx + (int64_t)t0 * keep, keep, p.R,
-          static_cast<uint32_t*>(ws) + (int64_t)t0 * p.groups * p.segs);
+          marks + (int64_t)t0 * p.groups * p.segs, turns + (int64_t)t0 * p.groups);
     }
     return true;
   };

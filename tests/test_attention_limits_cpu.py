@@ -86,3 +86,13 @@ def test_attention_refuses_a_selection_without_columns(M):
     assert zeros(3, 0).data_ptr() == 0
     with pytest.raises(ValueError, match="idx must be"):
         M.misa_kv4_attention(q, pool, zeros(3, 4), zeros(3), idx=zeros(3, 0))
+
+
+def test_workspace_of_closing_up_holds_marks_and_counters(lib):
+    """A mark for each segment of rows and a counter for each sequence and group that hands segments out."""
+    ws = lib.misa_workspace_bytes
+    for T, Hkv, d, keep in ((1, 1, 64, 40), (3, 8, 128, 20000), (16, 8, 128, 8192), (70000, 1, 64, 600)):
+        need = ws(12, T, 0, Hkv, 0, d, keep, 0)
+        assert need % 4 == 0 and need >= 2 * 4 * T, (T, keep)  # one segment and one counter at least
+        keys = ws(13, T, 0, 0, 0, 256, keep, 0)
+        assert keys % 4 == 0 and keys >= 2 * 4 * T

@@ -117,3 +117,38 @@ def test_values_that_are_not_finite_in_neighbouring_prompts(junk, d, Hq, Hkv, S,
         assert torch.equal(torch.nan_to_num(out.float(), nan=-7e9, posinf=7e9), torch.nan_to_num(want.float(), nan=-7e9, posinf=7e9))
         assert torch.equal(lse, gl)
     M.misa_device_check()
+
+
+@pytest.mark.parametrize("T,Hkv,d,page,L,keep", [
+    (1, 1, 64, 16, 60000, 59000),     # rows move a little: every segment's place is read by its neighbour
+    (1, 8, 128, 64, 40000, 39990),
+    (24, 2, 128, 32, 9000, 8000),     # more segments than run at once, of many sequences
+])
+def test_closing_up_where_every_segment_waits_for_its_neighbours(T, Hkv, d, page, L, keep):
+    M = lib()
+    gen = torch.Generator("cuda").manual_seed(keep)
+    per = -(-L // page)
+    table = torch.randperm(T * per, device="cuda", generator=gen).int().view(T, per)
+    pool = torch.randint(0, 256, (T * per, Hkv, 2, page * 9 * d // 16), device="cuda", dtype=torch.uint8, generator=gen)
+    keys = torch.randn(T * per, page, 128, device="cuda", generator=gen)
+    drop = torch.rand(T, L, device="cuda", generator=gen).argsort(1)[:, :L - keep]
+    stay = torch.ones(T, L, dtype=torch.bool, device="cuda").scatter_(1, drop, False)
+    idx = stay.nonzero()[:, 1].view(T, keep).int().contiguous()
+
+    def split(p):
+        a, b = p[..., :page * d // 2].unflatten(-1, (page, d // 2)), p[..., page * d // 2:].unflatten(-1, (page, d // 16))
+        return [x[table.long()].permute(0, 1, 4, 2, 3, 5).reshape(T, per * page, -1) for x in (a, b)]
+
+    before, kb = split(pool), keys[table.long()].view(T, per * page, 128)
+    for _ in range(2):  # the closed-up cache closes up once more
+        M.misa_kv4_compact(pool, table, idx, d)
+        after = split(pool)
+        for got, old in zip(after, before):
+            for t in range(T):
+                assert torch.equal(got[t, :keep], old[t, idx[t].long()]) and torch.equal(got[t, keep:], old[t, keep:])
+        before = after
+    M.misa_keys_compact_paged(keys, table, idx)
+    got = keys[table.long()].view(T, per * page, 128)
+    for t in range(T):
+        assert torch.equal(got[t, :keep], kb[t, idx[t].long()]) and torch.equal(got[t, keep:], kb[t, keep:])
+    M.misa_device_check()
