@@ -393,7 +393,8 @@ misa_status misa_kv4_read(const void* pool, int64_t num_pages, int page_size, co
  *   acc_opt    : [T][ld_acc] fp32, or NULL: acc[t][i] += sum over the H_q heads of token i's softmax
  *                weight (ld_acc >= L; other entries are not touched)
  *   ws         : misa_workspace_bytes(MISA_OP_KV4_ATTENTION, T, L, H_q, H_kv, d, P or 0, 1 with acc_opt
- *                else 0) bytes; with acc_opt it holds the logits, 4 H_q bytes per query and token
+ *                else 0) bytes; with acc_opt it holds the logits, 4 H_q bytes per query and token, of as many
+ *                queries at a time as 1 GiB holds (one at least)
  */
 misa_status misa_kv4_attention(const void* q, const void* pool, int64_t num_pages, int page_size,
                                const int32_t* page_table, int64_t max_pages, const int32_t* n, const int32_t* idx,

@@ -51,7 +51,10 @@ constexpr int kUnit = kWarps * kTile;  // tokens of a CTA's step: the grain of t
 // item to the next end last (64 queries of up to 16K tokens: 112 us, with one 104, two 102, four 104).  Units of
 // selected tokens take longer, and each CTA few of them (2048 of 32 queries: 63 us without, 69 with two).
 __host__ __device__ constexpr uint32_t item_cost(bool selected) { return selected ? 0u : 2u; }
-constexpr int kMaxT = 256;             // queries per launch
+constexpr int kMaxT = 256;             // queries per launch,
+// fewer where their logits, kept to sum weights, would take more than this (those of 256 queries of 64 heads over
+// 128K tokens take 8 GiB, which a workspace then keeps)
+constexpr size_t kLogitBytes = (size_t)1 << 30;
 constexpr int kMaxCtas = 1024;         // bound on the grid, for workspace sizes that ask no device
 // Weights are kept scaled by 2^kLift against the running maximum, which may lag the true one by
 // 2^kSlack: 2^15 at most, and what fp16 loses at the bottom lies below 2^-35 of the largest weight.
@@ -863,17 +866,27 @@ void launch_attn(const AttnArgs& a, float* acc, int cols, int64_t ld_acc, int64_
   }
 }
 
+// Positions that a query's logits have room for.
+int64_t logit_row(int P) { return ((int64_t)P + kUnit - 1) / kUnit * kUnit; }
+
+// Queries of a launch.
+int queries_per_launch(int T, int P, int Hq, bool weights) {
+  int64_t most = kMaxT;
+  if (weights) most = std::min<int64_t>(most, std::max<int64_t>(1, kLogitBytes / (sizeof(float) * Hq * logit_row(P))));
+  return (int)std::min<int64_t>(T, most);
+}
+
 }  // namespace
 
 size_t kv4_attention_ws_bytes(int T, int P, int Hq, int Hkv, int d, bool weights) {
   const int G = Hq / Hkv, HB = heads_per_item(G);
-  const int Tc = T < kMaxT ? T : kMaxT;
+  const int Tc = queries_per_launch(T, P, Hq, weights);
   const int64_t slots = kMaxCtas + (int64_t)Tc * Hkv * ((G + HB - 1) / HB);
   size_t b = up256(sizeof(uint64_t) * (kMaxT + 1)) + up256(sizeof(float) * slots * HB * d) +
              up256(sizeof(float) * slots * HB * 2);
   if (weights)
     b += up256(sizeof(float) * (size_t)Tc * Hq) +
-         up256(sizeof(float) * (size_t)Tc * Hq * (((size_t)P + kUnit - 1) / kUnit * kUnit));
+         up256(sizeof(float) * (size_t)Tc * Hq * logit_row(P));
   return b;
 }
 
@@ -882,8 +895,9 @@ void launch_kv4_attention(DType dt, const void* q, const Kv4Pool& pool, const in
                           float* acc, int acc_cols, int64_t ld_acc, void* ws, cudaStream_t s) {
   const int G = Hq / pool.Hkv, HB = heads_per_item(G);
   const size_t elt = dt == DType::BF16 ? 2 : 4;
-  for (int t0 = 0; t0 < T; t0 += kMaxT) {
-    const int Tc = T - t0 < kMaxT ? T - t0 : kMaxT;
+  const int most = queries_per_launch(T, P, Hq, acc != nullptr);
+  for (int t0 = 0; t0 < T; t0 += most) {
+    const int Tc = std::min(T - t0, most);
     AttnArgs a;
     a.q = static_cast<const char*>(q) + elt * t0 * (size_t)Hq * pool.d;
     a.pool = pool;
@@ -919,7 +933,7 @@ void launch_kv4_attention(DType dt, const void* q, const Kv4Pool& pool, const in
       a.lse2 = reinterpret_cast<float*>(p);
       p += up256(sizeof(float) * (size_t)Tc * Hq);
       a.logits = reinterpret_cast<float*>(p);
-      a.ldS = (a.P + kUnit - 1) / kUnit * (int64_t)kUnit;
+      a.ldS = logit_row(a.P);
       ac = acc + (int64_t)t0 * ld_acc;
     }
     const bool f32 = dt == DType::F32;

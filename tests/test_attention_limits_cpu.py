@@ -97,3 +97,14 @@ def test_workspace_of_closing_up_holds_marks_and_counters(lib):
         assert need % 4 == 0 and need >= words * 4 * T, (T, keep)
         keys = ws(13, T, 0, 0, 0, 256, keep, 0)
         assert keys % 4 == 0 and keys >= words * 4 * T
+
+
+def test_workspace_of_summed_weights_is_bounded(lib):
+    """The logits of as many queries as 1 GiB holds, one at least; never more than the call's own."""
+    ws = lib.misa_workspace_bytes
+    for T, L, Hq, Hkv in ((256, 131072, 64, 8), (4096, 131072, 128, 1), (256, 1 << 20, 8, 8)):
+        plain, weights = ws(11, T, L, Hq, Hkv, 128, 0, 0), ws(11, T, L, Hq, Hkv, 128, 0, 1)
+        one = 4 * Hq * (L + 128)
+        assert max(1 << 29, one) < weights <= plain + max(1 << 30, one) + 4 * 256 * Hq + 4096, (T, L, Hq)
+    assert ws(11, 16, 131072, 64, 8, 128, 0, 1) >= 16 * 131072 * 64 * 4  # half a GiB: in one go
+    assert ws(11, 1, 1 << 24, 256, 1, 128, 0, 1) >= (1 << 24) * 256 * 4  # a single query always

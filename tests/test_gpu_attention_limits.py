@@ -152,3 +152,32 @@ def test_closing_up_where_every_segment_waits_for_its_neighbours(T, Hkv, d, page
     for t in range(T):
         assert torch.equal(got[t, :keep], kb[t, idx[t].long()]) and torch.equal(got[t, keep:], kb[t, keep:])
     M.misa_device_check()
+
+
+@pytest.mark.parametrize("selected", [False, True])
+def test_more_weights_than_one_launch_keeps(selected):
+    """Logits past 1 GiB go in several launches: every query's output and sums are its own."""
+    M = lib()
+    rng = np.random.default_rng(8)
+    T, Hq, d, page, L = 40, 128, 64, 64, 65536
+    pool, one, _, gen = serving_state(M, [L], page, L // page, 1, d, 8)
+    table = one.expand(T, -1).contiguous()  # one sequence, read by every query
+    q = torch.randn(T, Hq, d, device="cuda", generator=gen).bfloat16()
+    n = cuda(rng.integers(1, L + 1, T).astype(np.int32))
+    n[0], n[31], n[32], n[39] = L, 1000, L, 0
+    pick = None
+    if selected:
+        pick = torch.stack([torch.randperm(L, device="cuda", generator=gen) for _ in range(T)]).int()
+    acc = torch.zeros(T, L, device="cuda")
+    out, lse = M.misa_kv4_attention(q, pool, table, n, idx=pick, acc=acc, want_lse=True)
+    for t in (0, 1, 30, 31, 32, 33, 39):  # alone: cut into other pieces, so equal up to rounding
+        a = torch.zeros(1, L, device="cuda")
+        o, z = M.misa_kv4_attention(q[t:t + 1], pool, one, n[t:t + 1].clone(), idx=None if pick is None else pick[t:t + 1],
+                                    acc=a, want_lse=True)
+        # weights in fp16 (2^-11 of sums of |v| below 1, either way), rounded to bf16 at the end (2^-8, either way);
+        # the sum of a lane's weights takes up to 2^8 additions of 2^-24, either way, its exponentials add 2^-19
+        assert (out[t].float() - o[0].float()).abs().max() <= 2 * 2.0 ** -8 * o.float().abs().max() + 2.0 ** -10
+        both = torch.isinf(z[0]) & torch.isinf(lse[t])
+        assert ((lse[t] - z[0]).abs() <= 2.0 ** -16 * z[0].abs() + 2.0 ** -14)[~both].all()
+        assert (acc[t] - a[0]).abs().max() <= 2.0 ** -14 * a.max() and (acc[t, int(n[t]):] == 0).all()
+        assert abs(float(acc[t].double().sum()) - (Hq if int(n[t]) else 0)) <= 2.0 ** -14 * Hq
