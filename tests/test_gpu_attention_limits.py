@@ -181,3 +181,41 @@ def test_more_weights_than_one_launch_keeps(selected):
         assert ((lse[t] - z[0]).abs() <= 2.0 ** -16 * z[0].abs() + 2.0 ** -14)[~both].all()
         assert (acc[t] - a[0]).abs().max() <= 2.0 ** -14 * a.max() and (acc[t, int(n[t]):] == 0).all()
         assert abs(float(acc[t].double().sum()) - (Hq if int(n[t]) else 0)) <= 2.0 ** -14 * Hq
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,Hq,Hkv,pick", [(128, 16, 2, None), (64, 12, 4, None), (128, 8, 1, 70), (64, 32, 2, 130)])
+@pytest.mark.parametrize("top,kg,vg", [
+    (0x07, 2.0 ** 9, 2.0 ** 8),      # zeros and the numbers below e4m3's normal range alone
+    (0x10, 100.0, 37.0),             # both sides of its border
+    (0x40, 0.4, 1.0),                # zero to 2
+])
+def test_attention_over_scales_below_the_normal_range(dtype, d, Hq, Hkv, pick, top, kg, vg):
+    M = lib()
+    rng = np.random.default_rng(top + d)
+    page, lens = 32, [300, 1, 129]
+    T, per = len(lens), 10
+    pool = rng.integers(0, 256, (T * per, Hkv, 2, page * 9 * d // 16), dtype=np.uint8)
+    _, scales = R.views(pool, page, d)
+    scales[...] = rng.integers(0, top + 1, scales.shape)
+    table = rng.permutation(T * per).reshape(T, per).astype(np.int32)
+    q = cuda(rng.standard_normal((T, Hq, d)).astype(np.float32), torch.bfloat16 if dtype == "bf16" else None)
+    idx = None
+    if pick:
+        idx = np.full((T, pick), -1, np.int32)
+        for t, n in enumerate(lens):
+            got = rng.permutation(n)[:pick]
+            idx[t, :len(got)] = got
+    out, lse = M.misa_kv4_attention(q, cuda(pool), cuda(table), cuda(np.array(lens, np.int32)),
+                                    idx=None if idx is None else cuda(idx), k_scale=kg, v_scale=vg, want_lse=True)
+    for t, n in enumerate(lens):
+        pos = np.arange(n) if idx is None else idx[t][idx[t] >= 0]
+        k, v = R.cache_rows(pool, table[t], pos, page, d)
+        k, v = k * float(np.float32(kg)), v * float(np.float32(vg))
+        qh = host(q[t:t + 1].float()).astype(np.float64)
+        want, z, p = R.attend(qh, k, v, d ** -0.5)
+        # weights: fp16 for bf16 outputs (half a step, 2^-11), two fp16 parts for fp32 ones; fp16 steps by 2^-24
+        # below its normal range, of weights scaled by 2^11 against the largest: 2^-36
+        tol, e = R.attend_tolerance(qh, k, v, d ** -0.5, p, dtype, 2.0 ** -11 if dtype == "bf16" else 2.0 ** -21, 2.0 ** -36)
+        assert np.all(np.abs(host(out[t].float()) - want[0]) <= tol[0])
+        assert np.all(np.abs(host(lse[t]) - z[0]) <= e + 2.0 ** -23 * np.abs(z[0]) + 2.0 ** -24 * max(16, len(pos)) + 2.0 ** -20)
