@@ -345,7 +345,7 @@ misa_status misa_hier_topk_fused(const void* q, const float* w, const void* k, i
  * Packed rows.  cu [S + 1] and, where a cache is involved, start [S] (int32, on the device) say which
  * rows of a packed tensor belong to which sequence: row r of sequence b, cu[b] <= r < cu[b + 1], is
  * its logical position start[b] + r - cu[b].  cu must not decrease and cu[0] >= 0; a sequence may be
- * empty.  Rows outside [cu[0], cu[S]) are neither read nor written.
+ * empty.  Rows outside [cu[0], cu[S]) are not written, and nothing depends on what they hold.
  *
  * Caches in 4 bits.  Every 16 elements of a row share a scale; an element is one of the 16 e2m1 values
  * (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign) times it:
@@ -356,8 +356,9 @@ misa_status misa_hier_topk_fused(const void* q, const float* w, const void* k, i
  * elements as the largest value).  A block whose scale rounds to 0 stores zeros.
  *   pool       : uint8 [num_pages][H_kv][2][page_size * 9 d / 16], 16-byte aligned; the slab of one
  *                page, kv head and side (0 keys, 1 values) holds page_size code rows of d/2 bytes and
- *                behind them page_size scale rows of d/16 e4m3 bytes.  Byte (d/8) c + 2 j + i of a code row
- *                holds elements 16 j + 4 c + 2 i (low nibble) and the next (c < 4, j < d/16, i < 2).
+ *                behind them page_size scale rows of d/16 e4m3 bytes, 0 to 0x7e (other scale bytes are none of
+ *                the format's; what attended rows with them give is not said).  Byte (d/8) c + 2 j + i of a
+ *                code row holds elements 16 j + 4 c + 2 i (low nibble) and the next (c < 4, j < d/16, i < 2).
  *   page_size  : a multiple of 16, at most 1024 (else MISA_ERR_UNSUPPORTED)
  *   page_table : [S or T][max_pages] int32, as for the paged key caches; the same tables can serve
  *                both.  Ids outside [0, num_pages) are never dereferenced: rows are not written, read
@@ -385,7 +386,8 @@ misa_status misa_kv4_read(const void* pool, int64_t num_pages, int page_size, co
 /*
  * Attention of one query token per sequence over its 4-bit cache:
  *   out[t, h] = sum_i softmax_i(scale q[t, h] . k_i) v_i   over i < n_t, or over i in idx[t].
- *   q, out     : [T][H_q][d], dtype (bf16, or fp32 computed to fp32's accuracy); 16-byte aligned
+ *   q, out     : [T][H_q][d], dtype; 16-byte aligned.  bf16 queries enter the products as they are; fp32 ones, and
+ *                their softmax weights, as two fp16 parts (22 bits); sums are fp32
  *   idx        : [T][P] tokens to attend to, in any order (misa_score_topk and the other selections
  *                write such lists), or NULL for the whole prefix.  Entries < 0 or >= n_t are empty slots;
  *                a token named twice counts twice.
@@ -430,9 +432,9 @@ misa_status misa_evict_select(const float* acc, int64_t ld_acc, const int32_t* n
 /*
  * Closes up caches after misa_evict_select, in place: row idx[t][j] of sequence t moves to row j, for
  * the 4-bit cache or the indexer's paged keys (pool [num_pages][page_size][128] of dtype).  idx ascends
- * strictly, with -1 behind the last, as misa_evict_select writes it.  Rows from the number kept on keep
- * their contents; block means of the keys are pooled again with misa_pool_keys_paged.  The pages of the
- * T sequences must be theirs alone.
+ * strictly, with -1 behind the last, as misa_evict_select writes it; keep is at most what the tables reach
+ * (max_pages * page_size).  Rows from the number kept on keep their contents; block means of the keys are
+ * pooled again with misa_pool_keys_paged.  The pages of the T sequences must be theirs alone.
  *   ws : misa_workspace_bytes(MISA_OP_KV4_COMPACT, T, 0, H_kv, 0, d, keep, 0), and
  *        misa_workspace_bytes(MISA_OP_KEYS_COMPACT_PAGED, T, 0, 0, 0, bytes of a key row, keep, 0) bytes
  *        (marks of which rows have been read, and counters of who reads which; cleared by the call)

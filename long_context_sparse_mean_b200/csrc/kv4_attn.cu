@@ -17,8 +17,8 @@
 // e2m1 x e4m3 has 6 significant bits and lies in fp16's range, so both operands are exact.
 // The query row is scaled by a power of two into fp16's upper range, where a bf16 row is exact down to
 // 2^-30 of its largest element; an fp32 row is split into two fp16 parts (22 bits), as are its weights.
-// Softmax weights are rounded to fp16 (2^-12) for the product with V where the output is bf16; the sums,
-// the maximum and the accumulators are fp32.
+// Softmax weights are rounded to fp16 (half a step: 2^-11 of the weight) for the product with V where the output
+// is bf16; the sums, the maximum and the accumulators are fp32.
 //
 // Work: every warp streams its own steps of 32 tokens through two buffers of asynchronous copies and keeps its
 // own running maximum, sum and output; the warps of a CTA join through shared memory, and the flattened (query,
@@ -26,12 +26,12 @@
 // where a piece ends inside a head's tokens.  Weights to be summed need the finished log-sums: the logits are
 // kept, and a third kernel turns them into weights.
 //
-// Measured: 16 queries of 64 heads over 120K to 128K tokens on 8 kv heads of d = 128 take 463 us, 5.0 TB/s of
-// cache (0.77 of the measured copy rate; 0.64 instructions a clock and scheduler: of 467 us, 393 without the copies,
-// 465 without the widening of K, 428 of V, 469 without the products).  Slower: five CTAs an SM at 96 registers 495, K
-// and V refilled by themselves 494, bulk copies of 128 bytes to 1 KB 561, of whole pages shared by two warps
-// 526.  32 queries of 32 heads over up to 16K tokens: 41 us, joins 8 and weights 10 us; 2048 selected tokens
-// of 32 queries (64 heads): 50 us for 75 MB in rows of 64 and 8 bytes from anywhere, joins 6, weights 9.
+// Measured: 16 queries of 64 heads over 120K to 128K tokens on 8 kv heads of d = 128 take 463 us by themselves, 5.0
+// TB/s of cache (0.77 of the measured copy rate), 526 us in a long run of calls on changing inputs; 0.64
+// instructions a clock and scheduler: of 467 us, 393 without the copies, 465 without the widening of K, 428 of V,
+// 469 without the products.  Slower: five CTAs an SM at 96 registers 495, K and V refilled by themselves 494, bulk
+// copies of 128 bytes to 1 KB 561, of whole pages shared by two warps 526.  32 queries of 32 heads over up to 16K tokens: 41 us, joins 8 and weights 10 us; 2048 selected
+// tokens of 32 queries (64 heads): 54 us with its joins for 75 MB in rows of 64 and 8 bytes from anywhere, 64 with the weights.
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -49,7 +49,9 @@ constexpr int kTile = 2 * kSub;        // tokens of a warp's step
 constexpr int kUnit = kWarps * kTile;  // tokens of a CTA's step: the grain of the split
 // Units that an item's start and end take as long as, for the even split: without them the CTAs that go from one
 // item to the next end last (64 queries of up to 16K tokens: 112 us, with one 104, two 102, four 104).  Units of
-// selected tokens take longer, and each CTA few of them (2048 of 32 queries: 63 us without, 69 with two).
+// selected tokens take longer, and each CTA few of them; which is better depends on the batch (2048 tokens of 64
+// heads on 8: 32 queries 53.6 us without, 55.8 with two, 16 queries 34.8 and 32.9, 8 queries 24.7 and 22.6; 1000 of
+// 32 heads on 4, 100 queries: 47.4 and 48.5), and large batches decided it.
 __host__ __device__ constexpr uint32_t item_cost(bool selected) { return selected ? 0u : 2u; }
 constexpr int kMaxT = 256;             // queries per launch,
 // fewer where their logits, kept to sum weights, would take more than this (those of 256 queries of 64 heads over
@@ -166,7 +168,8 @@ __device__ __forceinline__ void unit_prefix(const AttnArgs& a, uint64_t* pre, ui
 }
 
 // CTAs of an SM by registers: 128 a thread hold the state of 8 heads.  (96 and five CTAs also do without
-// spills for bf16, but took 495 us for 480 us at 16 x 128K tokens.)
+// spills for bf16, but took 495 us for 480 us at 16 x 128K tokens.)  The kernels of fp32 queries with d = 128 spill
+// 24 to 80 bytes a thread.
 __host__ __device__ constexpr int resident_ctas(int HB) { return HB == 16 ? 2 : 4; }
 
 template <int D, int NT, int SPLIT, bool GATHER>

@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(Kv4Pool pool, const int32
 // new place, and the segments waited for finished long ago.)  A short list is one segment and needs no marks.
 // Rows that stay where they are are passed over, and so are rows whose own or source page is not in the
 // pool.  Bound by HBM: rows are read and written once, but rows of 64 and 8 bytes from here and there fetch up
-// to twice their size.  16 caches of up to 32768 tokens thinned to 8192 (8 heads of 128): 60 us for 85 MB moved,
-// with 160 MB read; the indexer's bf16 keys beside them 19 us.  In chunks through workspace: 259 us.  (36 KB of
+// to twice their size.  16 caches of up to 32768 tokens thinned to 8192 (8 heads of 128): 65 us for 85 MB moved,
+// with 160 MB read (63 with segments by block index); the indexer's bf16 keys beside them 17 us.  In chunks through workspace: 259 us.  (36 KB of
 // rows in CTAs of 256 threads: one cache of 128K tokens 8 us faster, this batch 2 us slower.)
 // Waits are bounded (1 s); a segment whose wait runs out is not written and a status word is set.
 constexpr int kSeg = 64;                // fewest rows of a segment where there are several

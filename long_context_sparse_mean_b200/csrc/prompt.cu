@@ -11,7 +11,8 @@
 // would take 2048: Q K^T runs at 600 to 700 clocks for 512 (both operands come from shared memory, 128
 // bytes a clock, all it has), and a tile's own chain (scores, weights, P V, the next Q K^T) is as long as
 // that, because tensor memory has no room for a second set of scores.  4096 queries ending 32768 keys (16
-// heads on 2): 840 us, 1230 TFLOP/s, 0.74 of the measured bf16 rate.
+// heads on 2): 840 us by itself, 1230 TFLOP/s, 0.74 of the measured bf16 rate; in a long run of calls, under the
+// power cap, 953 us, 1080 TFLOP/s.
 // Tried and slower: scores of 64 keys in two halves, two steps ahead (1139 us for 838); a quarter to half
 // of the exponentials by a polynomial on the multiply-add units (860 to 927 for 858); reading the scores
 // twice from tensor memory instead of holding them (1073 for 1055); outputs through TMA stores.
@@ -58,6 +59,8 @@ constexpr int kRows = 128;                  // queries of a tile, keys of a bloc
 constexpr int kPair = 2 * kRows;            // queries of a CTA
 constexpr int kThreads = 12 * 32;
 // Registers a thread: 384 threads launch with 168 (64512 in all); 256 x 200 + 128 x 104 is the same.
+// The compiler spills 356 bytes stored and 480 loaded a thread at d = 128 (252 and 368 at d = 64), much of it in
+// the roles beside the softmax: 192 / 120 spills 248 and 320, 208 / 88 444 and 568.  200 / 104 is the one timed.
 constexpr int kRegsSoftmax = 200, kRegsOther = 104;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= 168 * kThreads, "register split exceeds the launch's registers");
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kGuardWarp = 10;
