@@ -219,3 +219,39 @@ def test_attention_over_scales_below_the_normal_range(dtype, d, Hq, Hkv, pick, t
         tol, e = R.attend_tolerance(qh, k, v, d ** -0.5, p, dtype, 2.0 ** -11 if dtype == "bf16" else 2.0 ** -21, 2.0 ** -36)
         assert np.all(np.abs(host(out[t].float()) - want[0]) <= tol[0])
         assert np.all(np.abs(host(lse[t]) - z[0]) <= e + 2.0 ** -23 * np.abs(z[0]) + 2.0 ** -24 * max(16, len(pos)) + 2.0 ** -20)
+
+
+def test_calls_with_given_outputs_and_workspace_allocate_nothing():
+    """Neither through the caching allocator nor beside it, once each kernel has run."""
+    M = lib()
+    T, Hq, Hkv, d, page, per, keep = 4, 16, 2, 128, 64, 40, 1500
+    pool, table, n, gen = serving_state(M, [per * page] * T, page, per, Hkv, d, 4)
+    cap = per * page
+    rows = 1000
+    pq, pk, pv = (torch.randn(rows, h, d, device="cuda", generator=gen).bfloat16() for h in (Hq, Hkv, Hkv))
+    cu, zero = cuda(np.array([0, 10, 700, rows], np.int32)), cuda(np.zeros(3, np.int32))
+    keys = torch.randn(T * per, page, 128, device="cuda", generator=gen).bfloat16()
+    acc, acc2 = torch.zeros(T, cap, device="cuda"), torch.zeros(T, cap, device="cuda")
+    q, idx = torch.randn(T, Hq, d, device="cuda", generator=gen).bfloat16(), torch.zeros(T, keep, dtype=torch.int32, device="cuda")
+    pout, plse, out, lse = torch.empty_like(pq), torch.empty(rows, Hq, device="cuda"), torch.empty_like(q), torch.empty(T, Hq, device="cuda")
+    kb, vb = torch.empty_like(pk), torch.empty_like(pv)
+    ws = M.Workspace()
+
+    def step():
+        M.misa_prompt_attention(pq, pk, pv, cu, out=pout, lse=plse, ws=ws)
+        M.misa_kv4_append(pk, pv, pool, table[:3], cu, zero)
+        M.misa_kv4_read(pool, table[:3], cu, zero, rows, d, k=kb, v=vb)
+        M.misa_kv4_attention(q, pool, table, n, out=out, lse=lse, acc=acc, ws=ws)
+        M.misa_kv4_attention(q, pool, table, n, idx=idx, out=out, ws=ws)
+        M.misa_evict_select(acc, n, keep, 4, 50, idx=idx, n_out=n, acc_out=acc2)
+        M.misa_kv4_compact(pool, table, idx, d, ws=ws)
+        M.misa_keys_compact_paged(keys, table, idx, ws=ws)
+
+    for _ in range(2):
+        step()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_stats()["allocation.all.allocated"], torch.cuda.mem_get_info()[0]
+    for _ in range(3):
+        step()
+    torch.cuda.synchronize()
+    assert (torch.cuda.memory_stats()["allocation.all.allocated"], torch.cuda.mem_get_info()[0]) == before
