@@ -238,11 +238,14 @@ class Workspace:
     hands its memory to no other tensor while that stream's kernels may still use it.  A call on
     another stream marks the buffer as used there too (record_stream, outside graph capture), so
     a buffer that is replaced later returns to the allocator only after the work of every stream
-    that used it."""
+    that used it.  A buffer that a captured call used is kept beside the one that replaces it, since the
+    graph uses it at every replay: a Workspace lives as long as the graphs that were captured with it."""
 
     def __init__(self, device=None):
         self.device = device
         self.buf = None
+        self._in_graph = False  # a captured call uses buf
+        self._kept = []  # replaced buffers that captured calls use
         self._home = None  # raw handle of the stream the buffer was allocated on
 
     def get(self, nbytes: int, stream=None) -> Optional[torch.Tensor]:
@@ -250,17 +253,25 @@ class Workspace:
             return None
         st = stream if stream is not None else torch.cuda.current_stream(self.device)
         if self.buf is None or self.buf.numel() < nbytes:
+            if self._in_graph:
+                self._kept.append(self.buf)
+                self._in_graph = False
             with torch.cuda.stream(st):
                 self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device or "cuda")
             self._home = int(st.cuda_stream)
         elif int(st.cuda_stream) != self._home and not torch.cuda.is_current_stream_capturing():
             self.buf.record_stream(st)
+        if torch.cuda.is_current_stream_capturing():
+            self._in_graph = True
         return self.buf
 
     def release(self) -> None:
-        """Drop the buffer (its memory goes back to torch's caching allocator)."""
+        """Drop the buffers (their memory goes back to torch's caching allocator); graphs that were captured
+        with this Workspace are not replayed after it."""
         self.buf = None
         self._home = None
+        self._in_graph = False
+        self._kept = []
 
 
 _default_ws = {}
@@ -283,7 +294,8 @@ def _ws(ws: Optional[Workspace], device, stream=None) -> Workspace:
 def release_default_workspaces() -> None:
     """Free every default workspace (for example after a run on many external streams, whose
     handles could otherwise be reused by unrelated streams that then inherit a large buffer).
-    Synchronises the device first, so no kernel still uses them."""
+    Synchronises the device first, so no kernel still uses them; graphs of calls that were captured
+    without a Workspace and do not keep their scratch themselves are not replayed after it."""
     if _default_ws:
         torch.cuda.synchronize()
     _default_ws.clear()
@@ -826,25 +838,31 @@ def _handle(stream, cur: int) -> int:
 _by_handle = {}  # (device index, stream handle) -> the default Workspace of that stream
 
 
+def _capturing(stream) -> bool:
+    """Whether a call on this stream (None: the current one) is being captured."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _scratch(ws: Optional["Workspace"], t: torch.Tensor, cur: int, nbytes: int, stream, handle: int):
     """nbytes of scratch for one call: the caller's Workspace, or the stream's default one, or, for a call
     that is captured without a Workspace, a buffer of the graph's own (two graphs that were captured on one
     stream may be replayed on two, and no later call can take the buffer away)."""
     if nbytes == 0:
         return None
+    capturing = _capturing(stream)
     if ws is None:
-        if stream is None:
-            if torch.cuda.is_current_stream_capturing():
-                return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-        else:
-            with torch.cuda.stream(stream):
-                if torch.cuda.is_current_stream_capturing():
-                    return torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+        if capturing:
+            return _new((nbytes,), torch.uint8, t.device, stream)
         ws = _by_handle.get((cur, handle))
         if ws is None:
             ws = _by_handle[(cur, handle)] = _ws(None, t.device, stream)
     if ws.buf is None or ws.buf.numel() < nbytes or ws._home != handle:
         ws.get(nbytes, stream)
+    if capturing:
+        ws._in_graph = True
     return ws.buf
 
 

@@ -108,3 +108,41 @@ def test_workspace_of_summed_weights_is_bounded(lib):
         assert max(1 << 29, one) < weights <= plain + max(1 << 30, one) + 4 * 256 * Hq + 4096, (T, L, Hq)
     assert ws(11, 16, 131072, 64, 8, 128, 0, 1) >= 16 * 131072 * 64 * 4  # half a GiB: in one go
     assert ws(11, 1, 1 << 24, 256, 1, 128, 0, 1) >= (1 << 24) * 256 * 4  # a single query always
+
+
+def test_a_workspace_keeps_the_buffers_that_captured_calls_use(M, monkeypatch):
+    """A graph writes to the scratch it was captured with at every replay, also after the workspace has grown."""
+    import contextlib
+    import gc
+    import types
+    import weakref
+
+    capturing = [False]
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=7))
+    monkeypatch.setattr(torch.cuda, "stream", lambda stream: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+
+    def get(ws, nbytes, capture, how):
+        capturing[0] = capture
+        if how == "get":
+            buf = ws.get(nbytes)
+        else:
+            buf = M._scratch(ws, torch.zeros(1), 0, nbytes, None, 7)
+        capturing[0] = False
+        return weakref.ref(buf)
+
+    for how in ("get", "scratch"):
+        ws = M.Workspace("cpu")
+        eager = get(ws, 1 << 10, False, how)
+        same = get(ws, 1 << 9, True, how)
+        assert same() is eager() is ws.buf
+        later = get(ws, 1 << 12, False, how)
+        gc.collect()
+        assert same() is not None and later() is not same(), how
+        grown = get(ws, 1 << 14, True, how)  # nothing captured used the one before
+        last = get(ws, 1 << 16, False, how)
+        gc.collect()
+        assert later() is None and grown() is not None and same() is not None and last() is ws.buf, how
+        ws.release()
+        gc.collect()
+        assert same() is None and grown() is None and last() is None and ws.buf is None

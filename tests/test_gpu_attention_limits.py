@@ -255,3 +255,35 @@ def test_calls_with_given_outputs_and_workspace_allocate_nothing():
         step()
     torch.cuda.synchronize()
     assert (torch.cuda.memory_stats()["allocation.all.allocated"], torch.cuda.mem_get_info()[0]) == before
+
+
+def test_a_graph_replays_after_its_workspace_has_grown():
+    """What a graph was captured with stays its own when a later, larger call replaces the workspace's buffer."""
+    M = lib()
+    Hq, Hkv, d, page, per = 16, 2, 128, 64, 16
+    pool, table, n, gen = serving_state(M, [per * page - 5, 700], page, per, Hkv, d, 9)
+    q = torch.randn(2, Hq, d, device="cuda", generator=gen).bfloat16()
+    acc, out, lse = torch.zeros(2, per * page, device="cuda"), torch.empty_like(q), torch.empty(2, Hq, device="cuda")
+    ws = M.Workspace()
+    call = lambda w: M.misa_kv4_attention(q, pool, table, n, out=out, lse=lse, acc=acc, ws=w)  # noqa: E731
+    call(ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(ws)
+    acc.zero_()
+    call(M.Workspace())
+    want = [x.clone() for x in (out, lse, acc)]
+    size = ws.buf.numel()
+    wide = torch.randn(200, 64, d, device="cuda", generator=gen).bfloat16()
+    rows = table[:1].expand(200, -1).contiguous()
+    M.misa_kv4_attention(wide, pool, rows, n[:1].expand(200).contiguous(), acc=torch.zeros(200, per * page, device="cuda"), ws=ws)
+    assert ws.buf.numel() > size
+    torch.cuda.synchronize()
+    others = [torch.full((size,), 0x5a, dtype=torch.uint8, device="cuda") for _ in range(4)]  # what a freed buffer would serve
+    for _ in range(3):
+        acc.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((out, lse, acc), want))
+        assert all((x == 0x5a).all() for x in others)
